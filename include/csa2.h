@@ -399,6 +399,215 @@ int csa2_decode_stack_noalloc(const csa2_layer *layers, int n_layers, const void
  * ------------------------------------------------------------------------ */
 int csa2_attn_resident_clusters(int heads_per_cluster);
 
+/* ========================================================================
+ * Paged FP4 cache. The pages describe one cache row per token; where a server
+ * keeps the rows of a sequence is left to it. The calls below hold the main-KV
+ * rows (and any other per-token buffers) in a pool of pages that sequences
+ * share, turn queries and rows by their rotary positions, and attend one new
+ * token over the pages.
+ *
+ *  pool        n_pages pages of page_size tokens: kv_fp4 [n_pages][page_size][C/2]
+ *              and kv_sf [n_pages][page_size][C/16] (MXFP4: [C/32]), the rows as
+ *              csa2_kv_append_fp4 writes them; further per-token buffers (indexer
+ *              keys, their scales) have the same page numbering.
+ *  page_table  [S][max_pages] int32: entry e of sequence s is the page of its
+ *              positions [e page_size, (e + 1) page_size), negative if there is
+ *              none. An entry outside [0, n_pages) counts as none in every call.
+ *  ref         [n_pages] int32: how many sequences hold the page; 0 = free.
+ *  page_size >= 1, max_pages >= 1, n_pages >= 1; page_size * max_pages and
+ *  n_pages * page_size below 2^40.
+ * A call over no rows, sequences or pairs is a no-op, whose arrays may be NULL.
+ * A page with ref > 1 is shared: nothing may append to it. csa2_pages_fork
+ * copies the one page of a fork that would be appended to.
+ * ======================================================================== */
+
+/* ------------------------------------------------------------------------
+ * Rotary positions. For token t, head h and pair i < rot_dim / 2, with
+ * a = pos[t] * inv_freq[i] (fp64), c = cos(a) * mscale, d = sin(a) * mscale
+ * (-sin when inverse != 0), and the pair's channels (relative to rot_start)
+ *   interleaved: u = 2i, v = 2i + 1;   half layout: u = i, v = i + rot_dim / 2:
+ *   out[u] = x[u] c - x[v] d,   out[v] = x[v] c + x[u] d   (fp32, rounded once).
+ * Channels outside [rot_start, rot_start + rot_dim) are copied. inverse
+ * gives the transposed map: the inverse when mscale is 1, and always the
+ * gradient of the forward call. K = V rows that carry the rotation give
+ * attention outputs that carry it too; the inverse call at the query's
+ * position takes it off.
+ *
+ *  x, out    [T][H][D] of dtype, channels contiguous; token and head strides in
+ *            elements, >= 0 (x_head_stride, out_head_stride >= D when H > 1).
+ *            out may be x with the same strides (in place: only the rotated
+ *            channels are touched); otherwise the two must not overlap.
+ *  pos       [T] int64 (device), any sign
+ *  inv_freq  [rot_dim / 2] fp64 (device): radians per position
+ *  dtype     CSA2_BF16 or CSA2_F32
+ *  rot_dim even, 2 <= rot_dim <= 1024, 0 <= rot_start <= D - rot_dim; H >= 1,
+ *  D <= 65536; T >= 0 (0 = nothing to do).
+ * ------------------------------------------------------------------------ */
+typedef enum csa2_dtype { CSA2_BF16 = 0, CSA2_F32 = 1 } csa2_dtype;
+typedef enum csa2_rope_layout { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALF = 1 } csa2_rope_layout;
+
+int csa2_rope(const void *x, void *out, int dtype, const int64_t *pos, const double *inv_freq,
+              int64_t T, int H, int D, int rot_start, int rot_dim, int layout, int inverse,
+              float mscale, int64_t x_tok_stride, int64_t x_head_stride, int64_t out_tok_stride,
+              int64_t out_head_stride, void *stream);
+
+/* The table csa2_rope reads: f_i = theta^(-2i / rot_dim), scaled for long contexts:
+ *  CSA2_ROPE_PLAIN   inv_freq[i] = f_i
+ *  CSA2_ROPE_LINEAR  inv_freq[i] = f_i / factor
+ *  CSA2_ROPE_YARN    inv_freq[i] = f_i (1 - r_i) + (f_i / factor) r_i with the ramp
+ *       r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *       lo = max(0, floor(n(beta_fast))), hi = min(rot_dim - 1, ceil(n(beta_slow))),
+ *       n(turns) = rot_dim ln(orig_ctx / (2 pi turns)) / (2 ln theta)
+ *     ("YaRN: Efficient Context Window Extension of Large Language Models",
+ *     section 3.2). Its attention factor, 0.1 ln(factor) + 1 on queries and on
+ *     keys, is csa2_rope's mscale.
+ *  theta > 1, factor >= 1; YARN also needs orig_ctx >= 1 and
+ *  beta_fast >= beta_slow > 0 (CSA2_ERR_RANGE otherwise). */
+typedef enum csa2_rope_scaling {
+    CSA2_ROPE_PLAIN = 0,
+    CSA2_ROPE_LINEAR = 1,
+    CSA2_ROPE_YARN = 2
+} csa2_rope_scaling;
+int csa2_rope_freqs(int rot_dim, double theta, int scaling, double factor, int64_t orig_ctx,
+                    double beta_fast, double beta_slow, double *inv_freq, void *stream);
+
+/* ------------------------------------------------------------------------
+ * FP4 append into pages: csa2_kv_append_fp4 (csa2_kv_append_mxfp4) with row
+ * (b, i) written at position p = start_pos[b] + i of sequence b, in page
+ * page_table[b][p / page_size], slot p % page_size. Bytes and scales are those
+ * calls' own. Rows with i >= n_valid[b], p < 0 or no page are skipped. Two rows
+ * that fall on the same slot leave one of them, which one is unspecified.
+ *
+ *  kv_bf16  [B][n_new][C] bf16, 16-byte aligned; start_pos [B] int64 (device)
+ *  n_valid  [B] int32 (device) or NULL (all n_new)
+ *  kv_fp4   8-byte aligned (the MXFP4 call: 16-byte); C as in the named calls
+ * ------------------------------------------------------------------------ */
+int csa2_paged_kv_append_fp4(const void *kv_bf16, int B, int n_new, int C, const int64_t *start_pos,
+                             const int32_t *n_valid, const int32_t *page_table, int max_pages,
+                             int page_size, int n_pages, uint8_t *kv_fp4, uint8_t *kv_sf,
+                             void *stream);
+int csa2_paged_kv_append_mxfp4(const void *kv_bf16, int B, int n_new, int C,
+                               const int64_t *start_pos, const int32_t *n_valid,
+                               const int32_t *page_table, int max_pages, int page_size, int n_pages,
+                               uint8_t *kv_fp4, uint8_t *kv_sf, void *stream);
+
+/* The rows back in bf16: out[b][i] = the dequantized row at position
+ * start_pos[b] + i, e2m1(code) * scale (exact in bf16 for E4M3 scales; for E8M0
+ * scales wherever the value is in bf16's range). Rows that the append would skip
+ * are left as they were.
+ *  out [B][n][C] bf16, 16-byte aligned; kv_fp4 8-byte aligned; C as above. */
+int csa2_paged_kv_gather_fp4(const uint8_t *kv_fp4, const uint8_t *kv_sf, const int32_t *page_table,
+                             int max_pages, int page_size, int n_pages, const int64_t *start_pos,
+                             const int32_t *n_valid, int B, int n, int C, void *out_bf16,
+                             void *stream);
+int csa2_paged_kv_gather_mxfp4(const uint8_t *kv_fp4, const uint8_t *kv_sf,
+                               const int32_t *page_table, int max_pages, int page_size, int n_pages,
+                               const int64_t *start_pos, const int32_t *n_valid, int B, int n, int C,
+                               void *out_bf16, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Page management. Every call is deterministic: free pages are taken in
+ * ascending order, for the first request first.
+ * ws/ws_bytes: at least csa2_pages_workspace_size(n_pages, n) bytes with n = S
+ * (extend), F (fork) or 0 (compact), 16-byte aligned; it need not be cleared and
+ * holds nothing between calls. Calls that may overlap need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+size_t csa2_pages_workspace_size(int n_pages, int n);
+
+/* Gives sequence s the pages of positions [0, want_len[s]): every entry
+ * e < ceil(want_len[s] / page_size) of its row that has none takes a free page
+ * (ref = 1), in the order of (s, e). Entries beyond max_pages and entries for
+ * which no page is left stay without; n_failed counts the latter.
+ *  want_len [S] int64 (device), n_failed [1] int32 (device). */
+int csa2_pages_extend(int32_t *page_table, int S, int max_pages, int32_t *ref, int n_pages,
+                      int page_size, const int64_t *want_len, int32_t *n_failed, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/* Fork f makes sequence dst[f] a continuation of src[f], whose first
+ * n = seq_len[src[f]] tokens it shares: dst takes src's pages of whole
+ * page_size tokens (ref + 1 each) and, when n % page_size tokens remain, a free
+ * page for them (ref = 1), with pairs[f] = (src's page, the new one) to be copied
+ * by csa2_pages_copy; pairs[f] = (-1, -1) when there is nothing to copy.
+ * seq_len[dst[f]] becomes n. If no free page is left, dst holds the whole pages
+ * alone, and seq_len[dst[f]] their tokens. A fork is refused, its dst left as it
+ * was and pairs[f] (-1, -1), if src[f] or dst[f] is outside [0, S), dst[f] is also
+ * a source of this call or the dst of an earlier f, or dst's row still holds a
+ * page. n_failed counts the refused forks and those without a free page.
+ *  seq_len [S] int64, src and dst [F] int32, pairs [F][2] int32, n_failed [1]
+ *  int32, all device. 0 <= F <= 65536. */
+int csa2_pages_fork(int32_t *page_table, int S, int max_pages, int32_t *ref, int n_pages,
+                    int page_size, int64_t *seq_len, const int32_t *src, const int32_t *dst, int F,
+                    int32_t *pairs, int32_t *n_failed, void *ws, size_t ws_bytes, void *stream);
+
+/* Takes the pages behind position keep_len[f] (all of them when keep_len is NULL)
+ * from sequence seq[f]: entries e >= ceil(keep_len[f] / page_size) become -1 and
+ * their pages' ref falls by one. A sequence may be listed more than once; one
+ * outside [0, S) is skipped.
+ *  seq [F] int32, keep_len [F] int64 or NULL, device. */
+int csa2_pages_free(int32_t *page_table, int S, int max_pages, int32_t *ref, int n_pages,
+                    int page_size, const int32_t *seq, const int64_t *keep_len, int F, void *stream);
+
+/* One per-token buffer of the cache: page p lies at base + p * page_bytes. */
+typedef struct csa2_page_buf {
+    void *base;
+    int64_t page_bytes;
+} csa2_page_buf;
+#define CSA2_MAX_PAGE_BUFS 16
+
+/* Copies page pairs[i][0] onto page pairs[i][1] in every buffer, i < F; pairs
+ * with a page outside [0, n_pages) are skipped. No destination may also be a
+ * source, or appear twice. pairs [F][2] int32 (device); bufs is a host array,
+ * read before the call returns; 1 <= n_bufs <= CSA2_MAX_PAGE_BUFS,
+ * page_bytes >= 1. */
+int csa2_pages_copy(const int32_t *pairs, int F, const csa2_page_buf *bufs, int n_bufs, int n_pages,
+                    void *stream);
+
+/* Moves the pages in use to the front of the pool: with L pages in use, the
+ * i-th page in use at or behind L moves to the i-th free page before L (both
+ * ascending), so that pages [0, L) are the ones in use and no more pages move
+ * than must. The data move in place in every buffer (a page that moved keeps its
+ * old bytes too); the table and the counts for the new places go to
+ * page_table_out and ref_out, which may be page_table and ref themselves.
+ * n_live receives L.
+ *  page_table, page_table_out [S][max_pages] int32; ref, ref_out [n_pages]
+ *  int32; n_live [1] int32; n_bufs may be 0 (tables only), bufs as above. */
+int csa2_pages_compact(const int32_t *page_table, int S, int max_pages, const int32_t *ref,
+                       int n_pages, const csa2_page_buf *bufs, int n_bufs, int32_t *page_table_out,
+                       int32_t *ref_out, int32_t *n_live, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of one new token over the pages. The query of sequence b is its
+ * token at position ctx_len[b] - 1, whose row is already in the pages, and sees
+ * the positions p < ctx_len[b] with
+ *   n_win = 0: every p;   n_win > 0: p >= ctx_len[b] - n_win or p < n_sink
+ * (a sliding window and the first tokens) that have a page. As in
+ * csa2_sparse_attn_decode K = V = the row, one KV head for all query heads:
+ *   s_j = softmax_scale * q[b][h] . row_j,  lse[b][h] = ln sum_j exp(s_j),
+ *   out[b][h] = sum_j exp(s_j - lse[b][h]) row_j.
+ * A query that sees no key gets a zero output and lse = -inf. Two calls over
+ * disjoint keys are joined by their lse.
+ *  q_bf16  [B][Hq][C] bf16, 16-byte aligned; out [B][Hq][C] bf16 (rounded once)
+ *  lse     [B][Hq] fp32 or NULL
+ *  ctx_len [B] int64 (device); above max_pages * page_size it counts as that
+ *  kv_fp4  16-byte aligned, kv_sf 4-byte aligned (MXFP4: any)
+ *  C % 32 == 0, 32 <= C <= 512; 1 <= Hq <= 256; n_win >= 0, n_sink >= 0
+ *  ws/ws_bytes: at least csa2_paged_attn_workspace_size(...) bytes, 16-byte
+ *  aligned; it starts with the call's error word (csa2_workspace_status), the
+ *  rest need not be cleared. Calls that may overlap, graphs among them, need
+ *  workspaces of their own.
+ * ------------------------------------------------------------------------ */
+size_t csa2_paged_attn_workspace_size(int B, int Hq, int C);
+int csa2_paged_attn_decode(const void *q_bf16, const uint8_t *kv_fp4, const uint8_t *kv_sf,
+                           const int32_t *page_table, int max_pages, int page_size, int n_pages,
+                           const int64_t *ctx_len, int64_t n_win, int64_t n_sink, int B, int Hq,
+                           int C, float softmax_scale, void *out_bf16, float *lse, void *ws,
+                           size_t ws_bytes, void *stream);
+int csa2_paged_attn_decode_mxfp4(const void *q_bf16, const uint8_t *kv_fp4, const uint8_t *kv_sf,
+                                 const int32_t *page_table, int max_pages, int page_size,
+                                 int n_pages, const int64_t *ctx_len, int64_t n_win, int64_t n_sink,
+                                 int B, int Hq, int C, float softmax_scale, void *out_bf16,
+                                 float *lse, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

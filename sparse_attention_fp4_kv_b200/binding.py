@@ -52,10 +52,15 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
 
 
 class csa2_layer(ctypes.Structure):
     _fields_ = [("mode", _I), ("q_idx", _P), ("q", _P), ("swa", _P), ("out", _P), ("topk", _P)]
+
+
+class csa2_page_buf(ctypes.Structure):
+    _fields_ = [("base", _P), ("page_bytes", _I64)]
 
 
 _SIGS = {
@@ -82,6 +87,25 @@ _SIGS = {
     "csa2_decode_stack_noalloc": (_I, [ctypes.POINTER(csa2_layer), _I, _P, _P, _P, _P, _P, _I64,
                                        _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _I, _P]),
     "csa2_attn_resident_clusters": (_I, [_I]),
+    "csa2_rope": (_I, [_P, _P, _I, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _F, _I64, _I64, _I64, _I64,
+                       _P]),
+    "csa2_rope_freqs": (_I, [_I, _D, _I, _D, _I64, _D, _D, _P, _P]),
+    "csa2_paged_kv_append_fp4": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "csa2_paged_kv_append_mxfp4": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "csa2_paged_kv_gather_fp4": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P]),
+    "csa2_paged_kv_gather_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P]),
+    "csa2_pages_workspace_size": (_SZ, [_I, _I]),
+    "csa2_pages_extend": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    "csa2_pages_fork": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "csa2_pages_free": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _I, _P]),
+    "csa2_pages_copy": (_I, [_P, _I, ctypes.POINTER(csa2_page_buf), _I, _I, _P]),
+    "csa2_pages_compact": (_I, [_P, _I, _I, _P, _I, ctypes.POINTER(csa2_page_buf), _I, _P, _P, _P,
+                                _P, _SZ, _P]),
+    "csa2_paged_attn_workspace_size": (_SZ, [_I, _I, _I]),
+    "csa2_paged_attn_decode": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _I64, _I64, _I, _I, _I, _F, _P,
+                                    _P, _P, _SZ, _P]),
+    "csa2_paged_attn_decode_mxfp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _I64, _I64, _I, _I, _I, _F,
+                                          _P, _P, _P, _SZ, _P]),
     "csa2_workspace_status": (_I, [_P, _I, _P]),
     "csa2_selftest_workspace_timeout": (_I, [_I, _P, _P]),
 }
@@ -316,3 +340,242 @@ class DecodeStack:
             ev = (_P * 2)(_P(scan_events[0].cuda_event), _P(scan_events[1].cuda_event))
         _check("csa2_decode_stack", lib.csa2_decode_stack(*self.args, ev, *self.ws_args,
                                                           _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- paged FP4 cache
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
+
+
+def _here(stream, *tensors):
+    """The paged calls launch on the stream's device (the current one without a
+    stream) and refuse tensors of another."""
+    dev = torch.cuda.current_device() if stream is None else stream.device.index
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the stream is on device {dev}, the current device is another")
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the call runs on device {dev}")
+
+
+def _scratch(nbytes: int, like, stream):
+    """Workspace of a call that was given none: allocated on the call's stream,
+    so that it is not handed out again before the call's kernels have run."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def csa2_rope_freqs(inv_freq, theta: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                    orig_ctx: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                    stream=None) -> None:
+    """inv_freq [rot_dim / 2] fp64: the table csa2_rope reads."""
+    _want(inv_freq, torch.float64, "inv_freq")
+    _here(stream, inv_freq)
+    _check("csa2_rope_freqs", lib.csa2_rope_freqs(
+        2 * inv_freq.numel(), float(theta), scaling, float(factor), orig_ctx, float(beta_fast),
+        float(beta_slow), _ptr(inv_freq), _stream(stream)))
+
+
+def csa2_rope(x, pos, inv_freq, out, rot_start: int = 0, interleaved: bool = True,
+              inverse: bool = False, mscale: float = 1.0, stream=None) -> None:
+    """x, out [T][H][D] bf16 or fp32 (out may be x; channels contiguous, any token
+    and head strides); pos [T] int64; inv_freq [rot_dim / 2] fp64. Rotates the
+    channels [rot_start, rot_start + rot_dim) of every head."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    _want(x, x.dtype, "x")
+    _want(out, x.dtype, "out")
+    _want(pos, torch.int64, "pos")
+    _want(inv_freq, torch.float64, "inv_freq")
+    T, H, D = x.shape
+    assert out.shape == x.shape and pos.shape == (T,) and inv_freq.dim() == 1
+    if D > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("the channels of x and out must be contiguous")
+    _here(stream, x, out, pos, inv_freq)
+    _check("csa2_rope", lib.csa2_rope(
+        _P(x.data_ptr()), _P(out.data_ptr()), int(x.dtype == torch.float32), _ptr(pos), _ptr(inv_freq),
+        T, H, D, rot_start, 2 * inv_freq.shape[0], 0 if interleaved else 1, int(inverse),
+        float(mscale), x.stride(0), x.stride(1), out.stride(0), out.stride(1), _stream(stream)))
+
+
+def _pool(kv_fp4, kv_sf, C: int, mx: bool):
+    """(page_size, n_pages) of a pool kv_fp4 [n_pages][page_size][C/2] and its scales."""
+    _want(kv_fp4, torch.uint8, "kv_fp4")
+    _want(kv_sf, torch.uint8, "kv_sf")
+    n_pages, page_size = kv_fp4.shape[:2]
+    assert kv_fp4.shape == (n_pages, page_size, C // 2)
+    assert kv_sf.shape == (n_pages, page_size, C // (32 if mx else 16))
+    return page_size, n_pages
+
+
+def csa2_paged_kv_append_fp4(kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid=None, stream=None,
+                             mx: bool = False) -> None:
+    """kv_bf16 [B][n_new][C] bf16; start_pos [B] int64; page_table [B][max_pages]
+    int32; kv_fp4 [n_pages][page_size][C/2] and kv_sf [..][C/16] (mx: [..][C/32])
+    uint8; n_valid [B] int32 or None."""
+    _want(kv_bf16, torch.bfloat16, "kv_bf16")
+    _want(start_pos, torch.int64, "start_pos")
+    _want(page_table, torch.int32, "page_table")
+    B, n, C = kv_bf16.shape
+    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
+    assert page_table.shape[0] == B and start_pos.shape == (B,)
+    if n_valid is not None:
+        _want(n_valid, torch.int32, "n_valid")
+        assert n_valid.shape == (B,)
+    _here(stream, kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    name = "csa2_paged_kv_append_mxfp4" if mx else "csa2_paged_kv_append_fp4"
+    _check(name, getattr(lib, name)(
+        _ptr(kv_bf16), B, n, C, _ptr(start_pos), _ptr(n_valid), _ptr(page_table), page_table.shape[1],
+        page_size, n_pages, _ptr(kv_fp4), _ptr(kv_sf), _stream(stream)))
+
+
+def csa2_paged_kv_gather(kv_fp4, kv_sf, page_table, start_pos, out, n_valid=None, stream=None,
+                         mx: bool = False) -> None:
+    """out [B][n][C] bf16 receives the rows at positions start_pos[b] + i; rows
+    with i >= n_valid[b] or no page are left as they were."""
+    _want(out, torch.bfloat16, "out")
+    _want(start_pos, torch.int64, "start_pos")
+    _want(page_table, torch.int32, "page_table")
+    B, n, C = out.shape
+    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
+    assert page_table.shape[0] == B and start_pos.shape == (B,)
+    if n_valid is not None:
+        _want(n_valid, torch.int32, "n_valid")
+        assert n_valid.shape == (B,)
+    _here(stream, out, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    name = "csa2_paged_kv_gather_mxfp4" if mx else "csa2_paged_kv_gather_fp4"
+    _check(name, getattr(lib, name)(
+        _ptr(kv_fp4), _ptr(kv_sf), _ptr(page_table), page_table.shape[1], page_size, n_pages,
+        _ptr(start_pos), _ptr(n_valid), B, n, C, _ptr(out), _stream(stream)))
+
+
+def pages_workspace_size(n_pages: int, n: int = 0) -> int:
+    return lib.csa2_pages_workspace_size(n_pages, n)
+
+
+def _pages_ws(ws, n_pages: int, n: int, ref, stream):
+    if ws is None:
+        ws = _scratch(pages_workspace_size(n_pages, n), ref, stream)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _want_pages(page_table, ref):
+    _want(page_table, torch.int32, "page_table")
+    _want(ref, torch.int32, "ref")
+    assert page_table.dim() == 2 and ref.dim() == 1
+
+
+def csa2_pages_extend(page_table, ref, want_len, page_size: int, n_failed, ws=None, stream=None) -> None:
+    """page_table [S][max_pages] int32; ref [n_pages] int32; want_len [S] int64;
+    n_failed [1] int32."""
+    _want_pages(page_table, ref)
+    _want(want_len, torch.int64, "want_len")
+    _want(n_failed, torch.int32, "n_failed")
+    S, M = page_table.shape
+    assert want_len.shape == (S,)
+    _here(stream, page_table, ref, want_len, n_failed, ws)
+    ws, wsb = _pages_ws(ws, ref.shape[0], S, ref, stream)
+    _check("csa2_pages_extend", lib.csa2_pages_extend(
+        _ptr(page_table), S, M, _ptr(ref), ref.shape[0], page_size, _ptr(want_len), _ptr(n_failed),
+        _ptr(ws), wsb, _stream(stream)))
+
+
+def csa2_pages_fork(page_table, ref, seq_len, src, dst, page_size: int, pairs, n_failed, ws=None,
+                    stream=None) -> None:
+    """seq_len [S] int64; src, dst [F] int32; pairs [F][2] int32; n_failed [1] int32."""
+    _want_pages(page_table, ref)
+    _want(seq_len, torch.int64, "seq_len")
+    for t, name in ((src, "src"), (dst, "dst"), (pairs, "pairs"), (n_failed, "n_failed")):
+        _want(t, torch.int32, name)
+    S, M = page_table.shape
+    F = src.shape[0]
+    assert seq_len.shape == (S,) and dst.shape == (F,) and pairs.shape == (F, 2)
+    _here(stream, page_table, ref, seq_len, src, dst, pairs, n_failed, ws)
+    ws, wsb = _pages_ws(ws, ref.shape[0], F, ref, stream)
+    _check("csa2_pages_fork", lib.csa2_pages_fork(
+        _ptr(page_table), S, M, _ptr(ref), ref.shape[0], page_size, _ptr(seq_len), _ptr(src), _ptr(dst), F,
+        _ptr(pairs), _ptr(n_failed), _ptr(ws), wsb, _stream(stream)))
+
+
+def csa2_pages_free(page_table, ref, seq, page_size: int, keep_len=None, stream=None) -> None:
+    """seq [F] int32; keep_len [F] int64 or None (nothing is kept)."""
+    _want_pages(page_table, ref)
+    _want(seq, torch.int32, "seq")
+    F = seq.shape[0]
+    if keep_len is not None:
+        _want(keep_len, torch.int64, "keep_len")
+        assert keep_len.shape == (F,)
+    _here(stream, page_table, ref, seq, keep_len)
+    _check("csa2_pages_free", lib.csa2_pages_free(
+        _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(ref), ref.shape[0], page_size,
+        _ptr(seq), _ptr(keep_len), F, _stream(stream)))
+
+
+def _page_bufs(bufs, n_pages: int):
+    """Tensors [n_pages][...] of one cache -> the C array of their bases and page sizes."""
+    arr = (csa2_page_buf * max(1, len(bufs)))()
+    for i, t in enumerate(bufs):
+        if not t.is_cuda:
+            raise ValueError("the cache buffers must be CUDA tensors")
+        assert t.shape[0] == n_pages
+        arr[i] = csa2_page_buf(_ptr(t), t[0].numel() * t.element_size())
+    return arr
+
+
+def csa2_pages_copy(pairs, bufs: Sequence[torch.Tensor], stream=None) -> None:
+    """pairs [F][2] int32 (from, onto); bufs: tensors [n_pages][...] of any dtype."""
+    _want(pairs, torch.int32, "pairs")
+    F = pairs.shape[0]
+    assert pairs.shape == (F, 2) and len(bufs) >= 1
+    n_pages = bufs[0].shape[0]
+    _here(stream, pairs, *bufs)
+    _check("csa2_pages_copy", lib.csa2_pages_copy(
+        _ptr(pairs), F, _page_bufs(bufs, n_pages), len(bufs), n_pages, _stream(stream)))
+
+
+def csa2_pages_compact(page_table, ref, bufs: Sequence[torch.Tensor], page_table_out, ref_out, n_live,
+                       ws=None, stream=None) -> None:
+    """page_table, page_table_out [S][max_pages] int32 and ref, ref_out [n_pages]
+    int32 (the outputs may be the inputs); bufs: tensors [n_pages][...]; n_live [1]
+    int32."""
+    _want_pages(page_table, ref)
+    _want_pages(page_table_out, ref_out)
+    _want(n_live, torch.int32, "n_live")
+    assert page_table_out.shape == page_table.shape and ref_out.shape == ref.shape
+    _here(stream, page_table, ref, page_table_out, ref_out, n_live, ws, *bufs)
+    ws, wsb = _pages_ws(ws, ref.shape[0], 0, ref, stream)
+    _check("csa2_pages_compact", lib.csa2_pages_compact(
+        _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(ref), ref.shape[0],
+        _page_bufs(bufs, ref.shape[0]), len(bufs), _ptr(page_table_out), _ptr(ref_out), _ptr(n_live),
+        _ptr(ws), wsb, _stream(stream)))
+
+
+def paged_attn_workspace_size(B: int, Hq: int, C: int) -> int:
+    return lib.csa2_paged_attn_workspace_size(B, Hq, C)
+
+
+def csa2_paged_attn_decode(q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, softmax_scale,
+                           n_win: int = 0, n_sink: int = 0, lse=None, ws=None, stream=None,
+                           mx: bool = False) -> None:
+    """q_bf16, out [B][Hq][C] bf16; kv_fp4 [n_pages][page_size][C/2] and kv_sf uint8;
+    page_table [B][max_pages] int32; ctx_len [B] int64; lse [B][Hq] fp32 or None;
+    n_win = 0 attends every position, else the last n_win and the first n_sink."""
+    _want(q_bf16, torch.bfloat16, "q_bf16")
+    _want(out, torch.bfloat16, "out")
+    _want(page_table, torch.int32, "page_table")
+    _want(ctx_len, torch.int64, "ctx_len")
+    B, Hq, C = q_bf16.shape
+    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
+    assert out.shape == q_bf16.shape and page_table.shape[0] == B and ctx_len.shape == (B,)
+    if lse is not None:
+        _want(lse, torch.float32, "lse")
+        assert lse.shape == (B, Hq)
+    _here(stream, q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, lse, ws)
+    if ws is None:
+        ws = _scratch(paged_attn_workspace_size(B, Hq, C), q_bf16, stream)
+    name = "csa2_paged_attn_decode_mxfp4" if mx else "csa2_paged_attn_decode"
+    _check(name, getattr(lib, name)(
+        _ptr(q_bf16), _ptr(kv_fp4), _ptr(kv_sf), _ptr(page_table), page_table.shape[1], page_size,
+        n_pages, _ptr(ctx_len), n_win, n_sink, B, Hq, C, float(softmax_scale), _ptr(out), _ptr(lse),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))

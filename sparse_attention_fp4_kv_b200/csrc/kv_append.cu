@@ -12,7 +12,7 @@
 // stores (8 B per lane) and scale stores (1 B per lane) are all coalesced.
 // The cost is negligible in decode (one row per sequence) and a few MB of
 // traffic in chunked prefill.
-#include "common.cuh"
+#include "kv_quant.cuh"
 
 namespace csa2 {
 
@@ -34,29 +34,10 @@ __device__ __forceinline__ void kv_append_group(const uint16_t *__restrict__ kv,
 
     const uint4 *src = reinterpret_cast<const uint4 *>(kv + row * C + (int64_t)g * 16);
     const uint4 a = src[0], c = src[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-    float x[16];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        x[2 * j] = bf16_lo(w[j]);
-        x[2 * j + 1] = bf16_hi(w[j]);
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(x[j]));
-
-    const uint32_t scode = f32_to_e4m3_satfinite(__fdiv_rn(amax, 6.0f));
-    const float s = e4m3_to_f32(scode);
-    uint32_t lo = 0, hi = 0;
-    if (s != 0.0f) {
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; j++) v[j] = __fdiv_rn(x[j], s);
-        lo = f32x8_to_e2m1x8(v);
-        hi = f32x8_to_e2m1x8(v + 8);
-    }
+    uint32_t scode;
+    const uint2 codes = fp4_quant16(a, c, scode);
     const int64_t cell = (int64_t)b * cap + pos;
-    *reinterpret_cast<uint2 *>(fp4 + cell * (C / 2) + (int64_t)g * 8) = make_uint2(lo, hi);
+    *reinterpret_cast<uint2 *>(fp4 + cell * (C / 2) + (int64_t)g * 8) = codes;
     sf[cell * G + g] = (uint8_t)scode;
 }
 
@@ -87,11 +68,7 @@ __global__ void __launch_bounds__(256) decode_step_begin_kernel(
     for (int64_t i = gid; i < n1; i += stride) z1[i] = make_uint4(0, 0, 0, 0);
 }
 
-// MXFP4 variant: one thread per 32-channel block. The shared exponent is the
-// exponent of the block's amax minus 2 (the largest E2M1 exponent), clamped to
-// the E8M0 range: read straight from the fp32 exponent field, so an all-zero or
-// subnormal amax gives 2^-127. Elements are x * 2^-e, an exact scaling since
-// the result stays below 8, then the same E2M1 pair conversion.
+// MXFP4 variant: one thread per 32-channel block (mxfp4_quant32).
 __global__ void __launch_bounds__(256) kv_append_mxfp4_kernel(
     const uint16_t *__restrict__ kv, int B, int n_new, int C, const int64_t *__restrict__ start_pos,
     int64_t pos_offset, int64_t cap, uint8_t *__restrict__ fp4, uint8_t *__restrict__ sf) {
@@ -109,34 +86,14 @@ __global__ void __launch_bounds__(256) kv_append_mxfp4_kernel(
     if (pos < 0 || pos >= cap) return;
 
     const uint4 *src = reinterpret_cast<const uint4 *>(kv + row * C + (int64_t)g * 32);
-    float x[32];
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-        const uint4 a = src[q];
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            x[8 * q + 2 * j] = bf16_lo(w[j]);
-            x[8 * q + 2 * j + 1] = bf16_hi(w[j]);
-        }
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 32; j++) amax = fmaxf(amax, fabsf(x[j]));
-    const int E = (int)((__float_as_uint(amax) >> 23) & 0xFF);  // 0 for zero / subnormal
-    int e = E == 0 ? -127 : E - 129;
-    e = e < -127 ? -127 : e;
-    // 2^-e as an fp32: e lies in [-127, 126], so 2^-e is a normal number
-    // (2^-126 .. 2^127)
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    float v[32];
-#pragma unroll
-    for (int j = 0; j < 32; j++) v[j] = x[j] * inv;
+    const uint4 a[4] = {src[0], src[1], src[2], src[3]};
+    uint32_t scode;
+    const uint4 codes = mxfp4_quant32(a, scode);
     const int64_t cell = (int64_t)b * cap + pos;
     uint2 *dst = reinterpret_cast<uint2 *>(fp4 + cell * (C / 2) + (int64_t)g * 16);
-    dst[0] = make_uint2(f32x8_to_e2m1x8(v), f32x8_to_e2m1x8(v + 8));
-    dst[1] = make_uint2(f32x8_to_e2m1x8(v + 16), f32x8_to_e2m1x8(v + 24));
-    sf[cell * G + g] = (uint8_t)(e + 127);
+    dst[0] = make_uint2(codes.x, codes.y);
+    dst[1] = make_uint2(codes.z, codes.w);
+    sf[cell * G + g] = (uint8_t)scode;
 }
 
 int launch_kv_append(const uint16_t *kv, int B, int n_new, int C, const int64_t *pos_base,

@@ -417,6 +417,9 @@ int csa2_attn_resident_clusters(int heads_per_cluster);
  *  page_size >= 1, max_pages >= 1, n_pages >= 1; page_size * max_pages and
  *  n_pages * page_size below 2^40.
  * A call over no rows, sequences or pairs is a no-op, whose arrays may be NULL.
+ * Bytes that no append writes (the NaN codes of the scales) are not values: a
+ * row that holds them gives unspecified results where it is read, and does no
+ * harm where it is not visible.
  * A page with ref > 1 is shared: nothing may append to it. csa2_pages_fork
  * copies the one page of a fork that would be appended to.
  * ======================================================================== */
@@ -586,7 +589,8 @@ int csa2_pages_compact(const int32_t *page_table, int S, int max_pages, const in
  *   out[b][h] = sum_j exp(s_j - lse[b][h]) row_j.
  * A query that sees no key gets a zero output and lse = -inf. Two calls over
  * disjoint keys are joined by their lse.
- *  q_bf16  [B][Hq][C] bf16, 16-byte aligned; out [B][Hq][C] bf16 (rounded once)
+ *  q_bf16  [B][Hq][C] bf16, 16-byte aligned; out [B][Hq][C] bf16, 8-byte aligned
+ *          (rounded once)
  *  lse     [B][Hq] fp32 or NULL
  *  ctx_len [B] int64 (device); above max_pages * page_size it counts as that
  *  kv_fp4  16-byte aligned, kv_sf 4-byte aligned (MXFP4: any)

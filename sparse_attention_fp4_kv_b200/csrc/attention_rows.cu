@@ -83,39 +83,6 @@ constexpr uint64_t WAIT_NS = 200ull * 1000 * 1000;
 
 __device__ int g_attn_rows_error = 0;
 
-// Non-blocking test and suspending try of an mbarrier phase of the given parity.
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-// try_wait with a suspend-time hint (ns): returns at the phase completion or
-// after about the hint.
-__device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity, uint32_t ns) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return done != 0;
-}
 __device__ __forceinline__ void raise_abort(volatile int *abort) {
     *abort = 1;
     atomicExch(&g_attn_rows_error, 1);
@@ -140,10 +107,6 @@ __device__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
         }
     }
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 __global__ void __launch_bounds__(THREADS, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tswa,
                      AttnArgs a, int n_sel_tiles, int n_win_tiles) {

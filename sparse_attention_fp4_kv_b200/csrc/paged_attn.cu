@@ -1,133 +1,170 @@
-// Attention of one new token over a paged FP4 cache.
-//
-// out = sum_j exp(s_j - m) row_j / sum_j exp(s_j - m), one pass over the keys
-// with the running maximum m and sum of each head in fp32. One CTA takes eight
-// heads of a sequence, a warp one head; tiles of 32 keys are dequantized to
-// shared memory once for the eight.
-#include "paged.cuh"
-
-#include <cuda_bf16.h>
+// Attention of one new token over a paged FP4 cache: the call, the kernel for
+// E4M3 scales (paged_attn.cuh), and the joining of a pair's parts.
+#include "paged_attn.cuh"
 
 namespace csa2 {
+
+int paged_attn_wait_flag(bool clear) { return read_device_flag(pa::g_paged_attn_error, clear); }
+
+int pa::launch_paged_attn_fp4(const Args &a, int nh, int G, cudaStream_t s) { return launch_attn<false>(a, nh, G, s); }
+
 namespace pa {
 
-constexpr int TK = 32, WARPS = 8, THREADS = WARPS * 32, MAX_C = 512;
-
-struct Args {
-    const uint16_t *q;
-    const uint8_t *fp4, *sf;
-    PagedKv pk;
-    const int64_t *ctx_len;
-    int64_t win, sink;
-    int B, Hq, C;
-    float scale;
-    uint16_t *out;
-    float *lse;
-    int *err;  // the call's error word
-};
-
-template <bool MX>
-__global__ void __launch_bounds__(THREADS) simple_kernel(const Args a) {
-    extern __shared__ float sm[];
-    const int pitch = a.C + 1;
-    float *tile = sm;                 // [TK][C + 1]
-    float *qs = sm + TK * pitch;      // [WARPS][C]
-    float *ps = qs + WARPS * a.C;     // [WARPS][TK]
-    __shared__ int ok[TK];
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
-    const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x * WARPS + warp;
-    int64_t n = a.ctx_len[b];
-    const int64_t cap = (int64_t)a.pk.max_pages * a.pk.page_size;
-    if (n > cap) n = cap;
-    if (n < 0) n = 0;
-    int64_t ns = 0, w0 = 0;
-    if (a.win > 0) {
-        ns = a.sink < n ? a.sink : n;
-        w0 = n - a.win > ns ? n - a.win : ns;
+// Joins the parts that the CTAs of a split (sequence, head group) pair left:
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. Block (pair, y) takes
+// `per` heads; its threads are columns of four channels times groups of parts, so
+// that many parts' loads are in flight. Pairs without a key get zeros here, pairs
+// within one CTA are already finished. Block (0, 0) also sets the error word.
+constexpr int JT = 512;
+constexpr int MAX_PARTS = 1024;  // CTAs of the attention kernel
+__global__ void __launch_bounds__(JT) join_kernel(const Args a, int NH, int pitch, int G, int per, int *err) {
+    __shared__ float weight[MAX_PARTS];
+    __shared__ float4 acc[JT];
+    __shared__ float red[2][JT / 32];
+    grid_dep_wait();
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        int any = 0;
+        for (int i = tid; i < G; i += JT) any |= a.flags[i];
+        any = __syncthreads_or(any);
+        if (tid == 0) *err = any != 0;
     }
-    const int64_t nvis = ns + n - w0;
-    if (h < a.Hq)
-        for (int c = lane; c < a.C; c += 32)
-            qs[warp * a.C + c] = __uint_as_float((uint32_t)a.q[((int64_t)b * a.Hq + h) * a.C + c] << 16);
-    float m = -INFINITY, l = 0.0f, o[MAX_C / 32];
-#pragma unroll
-    for (int i = 0; i < MAX_C / 32; i++) o[i] = 0.0f;
-    for (int64_t j0 = 0; j0 < nvis; j0 += TK) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < TK * (a.C / 2); i += THREADS) {
-            const int r = i / (a.C / 2), cb = i - r * (a.C / 2);
-            const int64_t j = j0 + r;
-            const int64_t row = j < nvis ? paged_row(a.pk, b, j < ns ? j : w0 + j - ns) : -1;
-            float lo = 0.0f, hi = 0.0f;
-            if (row >= 0) {
-                const uint32_t byte = a.fp4[row * (a.C / 2) + cb];
-                const float s = MX ? e8m0_to_f32(a.sf[row * (a.C / 32) + cb / 16])
-                                   : e4m3_to_f32(a.sf[row * (a.C / 16) + cb / 8]);
-                lo = e2m1_to_f32(byte & 15) * s;
-                hi = e2m1_to_f32(byte >> 4) * s;
-            }
-            tile[r * pitch + 2 * cb] = lo;
-            tile[r * pitch + 2 * cb + 1] = hi;
-            if (cb == 0) ok[r] = row >= 0;
+    const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+    const int64_t T = a.prefix[a.B] * a.groups, p0 = a.prefix[b], tiles = a.prefix[b + 1] - p0;
+    const int64_t t0 = p0 * a.groups + g * tiles;
+    const int sharers = sharing(T, G);
+    const int lo = tiles ? owner_of(t0, T, sharers) : 0, hi = tiles ? owner_of(t0 + tiles - 1, T, sharers) : 0;
+    if (tiles && lo == hi) return;
+    const int n = hi - lo + 1;
+    // the part of the first CTA: its second segment unless its share starts here
+    const int slot0 = 2 * lo + (tiles && share_begin(lo, T, sharers) != t0 ? 1 : 0);
+    auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (lo + i); };
+    const int cols = a.C / 4, col = tid % cols, grp = tid / cols, groups = JT / cols;
+    for (int y = 0; y < per; y++) {
+        const int hh = blockIdx.y * per + y, h = g * NH + hh;
+        if (hh >= NH || h >= a.Hq) break;
+        uint2 *out = reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.Hq + h) * a.C);
+        float *lse = a.lse ? a.lse + (int64_t)b * a.Hq + h : nullptr;
+        if (!tiles) {
+            if (tid < cols) out[tid] = make_uint2(0, 0);
+            if (tid == 0 && lse) *lse = -INFINITY;
+            continue;
         }
-        __syncthreads();
-        if (h >= a.Hq) continue;
-        float x = 0.0f;
-        for (int c = 0; c < a.C; c++) x += qs[warp * a.C + c] * tile[lane * pitch + c];
-        x = ok[lane] ? x * a.scale : -INFINITY;
-        float mt = x;
+        float m = REF_NONE;
+        for (int i = tid; i < n; i += JT) m = fmaxf(m, a.part_ml[((int64_t)slot(i) * NH + hh) * 2]);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
-        if (mt == -INFINITY) continue;
-        const float m_new = fmaxf(m, mt);
-        const float alpha = expf(m - m_new), p = expf(x - m_new);
-        float sum = p;
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if ((tid & 31) == 0) red[0][tid >> 5] = m;
+        __syncthreads();
+        for (int i = 0; i < JT / 32; i++) m = fmaxf(m, red[0][i]);
+        float sum = 0.0f;
+        for (int i = tid; i < n; i += JT) {
+            const float *ml = a.part_ml + ((int64_t)slot(i) * NH + hh) * 2;
+            const float wt = ex2(ml[0] - m);
+            weight[i] = wt;
+            sum += wt * ml[1];
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l = l * alpha + sum;
-        m = m_new;
-        ps[warp * TK + lane] = p;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < MAX_C / 32; i++) {
-            if (i * 32 >= a.C) break;
-            float v = o[i] * alpha;
-            for (int r = 0; r < TK; r++) v += ps[warp * TK + r] * tile[r * pitch + i * 32 + lane];
-            o[i] = v;
+        if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int i = 0; i < JT / 32; i++) sum += red[1][i];
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (grp < groups) {
+            const float *o = a.part_o + (int64_t)hh * pitch + 4 * col;
+#pragma unroll 8
+            for (int i = grp; i < n; i += groups) {
+                const float4 x = *reinterpret_cast<const float4 *>(o + (int64_t)slot(i) * NH * pitch);
+                const float wt = weight[i];
+                v.x += wt * x.x;
+                v.y += wt * x.y;
+                v.z += wt * x.z;
+                v.w += wt * x.w;
+            }
         }
-        __syncwarp();
+        acc[tid] = v;
+        __syncthreads();
+        if (tid < cols) {
+            for (int i = 1; i < groups; i++) {
+                const float4 x = acc[i * cols + tid];
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            out[tid] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+        }
+        if (tid == 0 && lse) *lse = sum != 0.0f ? (m - P_OFFSET + log2f(sum)) * LN2 : -INFINITY;
+        __syncthreads();
     }
-    if (h >= a.Hq) return;
-#pragma unroll
-    for (int i = 0; i < MAX_C / 32; i++) {
-        if (i * 32 >= a.C) break;
-        const __nv_bfloat16 v = __float2bfloat16_rn(l != 0.0f ? o[i] / l : 0.0f);
-        a.out[((int64_t)b * a.Hq + h) * a.C + i * 32 + lane] = *reinterpret_cast<const uint16_t *>(&v);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)b * a.Hq + h] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 
-template <bool MX>
-int decode(const void *q, const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_pages,
+// Heads of one group: the smallest MMA width that holds them, 64 at most.
+int group_heads(int Hq) { return Hq <= 16 ? 16 : Hq <= 32 ? 32 : 64; }
+
+constexpr size_t up(size_t x) { return (x + 255) / 256 * 256; }
+// Workspace: the error word, the CTAs' flags, the tiles before each sequence,
+// and two parts per CTA.
+struct Ws {
+    int *err, *flags;
+    int64_t *prefix;
+    float *ml, *o;
+    size_t bytes;
+};
+Ws layout(void *base, int B, int Hq, int C, int G) {
+    const int nh = group_heads(Hq), pitch = (C + 127) / 128 * 128;
+    char *p = static_cast<char *>(base);
+    size_t off = 0;
+    Ws w;
+    auto take = [&](size_t bytes) {
+        char *q = p + off;
+        off += up(bytes);
+        return q;
+    };
+    w.err = reinterpret_cast<int *>(take(sizeof(int)));
+    w.flags = reinterpret_cast<int *>(take(sizeof(int) * (size_t)G));
+    w.prefix = reinterpret_cast<int64_t *>(take(sizeof(int64_t) * ((size_t)B + 1)));
+    w.ml = reinterpret_cast<float *>(take(sizeof(float) * 2 * 2 * (size_t)G * nh));
+    w.o = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)G * nh * pitch));
+    w.bytes = off;
+    return w;
+}
+
+// One CTA per SM: the shared memory of one leaves no room for a second.
+int grid_ctas() {
+    const int n = num_sms();
+    return n < MAX_PARTS ? n : MAX_PARTS;
+}
+
+int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_pages,
            int page_size, int n_pages, const int64_t *ctx_len, int64_t n_win, int64_t n_sink, int B, int Hq,
            int C, float scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
     if (B != 0 && (!q || !fp4 || !sf || !table || !ctx_len || !out)) return CSA2_ERR_NULL;
-    if (B < 0 || Hq < 1 || Hq > 256 || C < 32 || C > MAX_C || C % 32 ||
+    if (B < 0 || Hq < 1 || Hq > 256 || C < 32 || C > 512 || C % 32 ||
         !paged_shape_ok(max_pages, page_size, n_pages))
         return CSA2_ERR_SHAPE;
     if (n_win < 0 || n_sink < 0) return CSA2_ERR_RANGE;
-    if (!aligned(q, 16) || !aligned(fp4, 16) || (!MX && !aligned(sf, 4))) return CSA2_ERR_ALIGN;
+    if (!aligned(q, 16) || !aligned(fp4, 16) || !aligned(out, 8) || (!mx && !aligned(sf, 4))) return CSA2_ERR_ALIGN;
     if (B == 0) return CSA2_OK;
-    if (!ws || ws_bytes < csa2_paged_attn_workspace_size(B, Hq, C)) return CSA2_ERR_WORKSPACE;
+    const int G = grid_ctas(), nh = group_heads(Hq), groups = (Hq + nh - 1) / nh;
+    if ((int64_t)B * groups > INT32_MAX) return CSA2_ERR_SHAPE;
+    const Ws w = layout(ws, B, Hq, C, G);
+    if (!ws || ws_bytes < w.bytes) return CSA2_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return CSA2_ERR_ALIGN;
-    static PerDevice smem_set;
-    const size_t smem = sizeof(float) * ((size_t)TK * (C + 1) + (size_t)WARPS * (C + TK));
-    if (!set_smem_limit_once(smem_set, simple_kernel<MX>, 100 * 1024)) return CSA2_ERR_CUDA;
-    const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len,
-                 n_win, n_sink, B, Hq, C, scale, (uint16_t *)out, lse, (int *)ws};
-    return launch_kernel(false, simple_kernel<MX>, dim3((unsigned)(Hq + WARPS - 1) / WARPS, (unsigned)B),
-                         dim3(THREADS), smem, (cudaStream_t)stream, a);
+    cudaStream_t s = (cudaStream_t)stream;
+    const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len, n_win,
+                 n_sink, B, Hq, C, groups, scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
+    const int st = mx ? launch_paged_attn_mxfp4(a, nh, G, s) : launch_paged_attn_fp4(a, nh, G, s);
+    if (st != CSA2_OK) return st;
+    // one head per block until there are a few blocks per SM
+    const int pairs = B * groups;
+    int blocks = 4 * G / pairs;
+    blocks = blocks < 1 ? 1 : blocks > nh ? nh : blocks;
+    const int per = (nh + blocks - 1) / blocks;
+    return launch_kernel(true, join_kernel, dim3((unsigned)pairs, (unsigned)((nh + per - 1) / per)), dim3(JT), 0,
+                         s, a, nh, (C + 127) / 128 * 128, G, per, w.err);
 }
 
 }  // namespace pa
@@ -135,7 +172,7 @@ int decode(const void *q, const uint8_t *fp4, const uint8_t *sf, const int32_t *
 
 extern "C" size_t csa2_paged_attn_workspace_size(int B, int Hq, int C) {
     if (B < 1 || Hq < 1 || C < 1) return 0;
-    return 256;
+    return csa2::pa::layout(nullptr, B, Hq, C, csa2::pa::grid_ctas()).bytes;
 }
 
 extern "C" int csa2_paged_attn_decode(const void *q_bf16, const uint8_t *kv_fp4, const uint8_t *kv_sf,
@@ -143,9 +180,8 @@ extern "C" int csa2_paged_attn_decode(const void *q_bf16, const uint8_t *kv_fp4,
                                       const int64_t *ctx_len, int64_t n_win, int64_t n_sink, int B, int Hq,
                                       int C, float softmax_scale, void *out_bf16, float *lse, void *ws,
                                       size_t ws_bytes, void *stream) {
-    return csa2::pa::decode<false>(q_bf16, kv_fp4, kv_sf, page_table, max_pages, page_size, n_pages, ctx_len,
-                                   n_win, n_sink, B, Hq, C, softmax_scale, out_bf16, lse, ws, ws_bytes,
-                                   stream);
+    return csa2::pa::decode(false, q_bf16, kv_fp4, kv_sf, page_table, max_pages, page_size, n_pages, ctx_len,
+                            n_win, n_sink, B, Hq, C, softmax_scale, out_bf16, lse, ws, ws_bytes, stream);
 }
 
 extern "C" int csa2_paged_attn_decode_mxfp4(const void *q_bf16, const uint8_t *kv_fp4, const uint8_t *kv_sf,
@@ -154,7 +190,6 @@ extern "C" int csa2_paged_attn_decode_mxfp4(const void *q_bf16, const uint8_t *k
                                             int64_t n_sink, int B, int Hq, int C, float softmax_scale,
                                             void *out_bf16, float *lse, void *ws, size_t ws_bytes,
                                             void *stream) {
-    return csa2::pa::decode<true>(q_bf16, kv_fp4, kv_sf, page_table, max_pages, page_size, n_pages, ctx_len,
-                                  n_win, n_sink, B, Hq, C, softmax_scale, out_bf16, lse, ws, ws_bytes,
-                                  stream);
+    return csa2::pa::decode(true, q_bf16, kv_fp4, kv_sf, page_table, max_pages, page_size, n_pages, ctx_len,
+                            n_win, n_sink, B, Hq, C, softmax_scale, out_bf16, lse, ws, ws_bytes, stream);
 }

@@ -1,0 +1,862 @@
+// Attention of one new token over a paged FP4 cache: the tensor-core kernel.
+// paged_attn.cu and paged_attn_mx.cu instantiate it for the two scale formats.
+//
+//   S^T[key, head]  = K Q^T        M = 128 keys, N = heads, K = channels
+//   O^T[chan, head] += V^T P^T     M = 128 channels, N = heads, K = 128 keys
+// with K = V = the dequantized rows. Keys and channels lie on the MMAs' 128 rows
+// because a decode query has 64 heads or fewer, and M = 64 runs at half rate.
+//
+// Work: every sequence is cut into tiles of 128 visible keys; the tiles of all
+// (sequence, head group) pairs form one list that is divided evenly over the
+// CTAs (one per SM), so that one long sequence and many short ones both fill the
+// card. A CTA walks its share with an online softmax and keeps O^T in tensor
+// memory; a pair that lies within one CTA is finished there, otherwise each CTA
+// leaves (m, l, O) of its part and the combine kernel joins them.
+//
+// Roles of the 17 warps:
+//   0-7   softmax: thread = key; warps 0-3 the first half of the heads, 4-7 the
+//         second. Also the epilogue.
+//   8-15  loads: codes and scales of the next tile in registers while the
+//         current one is dequantized to shared memory; the queries.
+//   16    one thread issues the MMAs, first P V of a tile whose weights are
+//         ready, else S of the next.
+// Shared memory holds a ring of units of 128 keys x 128 channels (32 KB); a
+// tile of C channels is ceil(C / 128) units, each read by S as K (K-major) and by
+// O as V (MN-major) from the same bytes.
+//
+// Softmax: out = sum 2^(x_j - r) v_j / sum 2^(x_j - r) for any reference r. r is
+// the head's maximum of its first tile and moves only when a score exceeds it
+// by 2^8, so almost every tile needs no reduction over keys: a thread checks its
+// own scores, one vote decides. l is kept per thread and summed over the keys
+// once per sequence.
+//
+// Types. E4M3 scales: e2m1 x e4m3 has at most 6 significant bits and is a
+// multiple of 2^-10 below 2^12, so f16 holds it exactly. Queries are bf16 (8
+// bits); scaled by a power of two per head that brings their largest element
+// to [2^13, 2^14) they are exact in f16 down to 2^-31 of that element, below which
+// they round at 2^-25 absolute (2^-38 of it). Weights are rounded to f16: 2^-11
+// relative, an eighth of the output's own bf16 rounding; they are kept below
+// 2^15 by an offset of 7 in the exponent, so that weights down to 2^-21 of the
+// reference keep all bits and those below 2^-32 vanish. E8M0 scales exceed f16's
+// range: rows and queries are bf16 (exact), and the weights are two bf16 parts
+// (16 bits), which costs a second P V.
+#pragma once
+
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace csa2 {
+namespace pa {
+
+struct Args {
+    const uint16_t *q;
+    const uint8_t *fp4, *sf;
+    PagedKv pk;
+    const int64_t *ctx_len;
+    int64_t win, sink;
+    int B, Hq, C, groups;  // groups of NH heads
+    float scale;
+    uint16_t *out;
+    float *lse;
+    // workspace
+    int *flags;        // [G] a CTA that gave up a wait
+    int64_t *prefix;   // [B + 1] tiles before sequence b
+    float *part_ml;    // [2 G][NH][2]
+    float *part_o;     // [2 G][NH][128 U]
+};
+
+constexpr int TK = 128;             // keys per tile
+constexpr int CHUNK = TK * 128;     // 64 channels of a tile: rows of 128 bytes
+constexpr int UNIT = 2 * CHUNK;
+constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 32;
+constexpr int MMA_WARP = (NSOFT + NLOAD) / 32;
+constexpr int MAX_RING = 6;
+constexpr int VALID_RING = 8, QF_RING = 4;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 8.0f;  // how far a score may exceed the reference
+constexpr float P_OFFSET = 7.0f;      // weights are 2^(x - r + 7) <= 2^15
+constexpr float REF_NONE = -3.0e38f;  // no key yet
+constexpr uint64_t WAIT_NS = 200ull * 1000 * 1000;
+
+// Visible keys of a sequence of n tokens: positions [0, ns) and [w0, n), listed
+// in that order.
+struct Seq {
+    int64_t nvis, ns, w0, tiles;
+};
+__device__ __forceinline__ Seq seq_of(const Args &a, int b) {
+    int64_t n = __ldg(a.ctx_len + b);
+    const int64_t cap = (int64_t)a.pk.max_pages * a.pk.page_size;
+    n = n > cap ? cap : n < 0 ? 0 : n;
+    Seq s;
+    s.ns = s.w0 = 0;
+    if (a.win > 0) {
+        s.ns = a.sink < n ? a.sink : n;
+        s.w0 = n - a.win > s.ns ? n - a.win : s.ns;
+    }
+    s.nvis = s.ns + n - s.w0;
+    s.tiles = (s.nvis + TK - 1) / TK;
+    return s;
+}
+
+// T tiles are shared by min(G, T) CTAs, so that none between two that have tiles
+// has none. First tile of CTA c's share, and the CTA of tile t.
+__device__ __forceinline__ int sharing(int64_t T, int G) { return T < G ? (int)T : G; }
+__device__ __forceinline__ int64_t share_begin(int c, int64_t T, int G) { return c * T / G; }
+__device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (int)(((t + 1) * G - 1) / T); }
+
+template <bool MX, int U, int NH>
+struct Layout {
+    static constexpr int PARTS = MX ? 2 : 1;       // of the weights
+    static constexpr int NP = (U == 4 && NH == 64) ? 1 : 2;  // buffers of weights
+    static constexpr int P_PART = TK * NH * 2;
+    static constexpr int Q_CHUNK = NH * 128;       // 64 channels of Q
+    static constexpr int Q_OFF = 0;
+    static constexpr int P_OFF = Q_OFF + 2 * U * Q_CHUNK;
+    static constexpr int K_OFF = P_OFF + NP * PARTS * P_PART;
+    static constexpr int SMALL = 3072;
+    static constexpr int FIT = (227 * 1024 - SMALL - K_OFF) / UNIT;
+    static constexpr int NU = FIT < MAX_RING ? FIT : MAX_RING;  // units of the ring
+    static_assert(NU >= U, "a tile fits the ring");
+    static constexpr int QF_OFF = K_OFF + NU * UNIT;      // fp32 [QF_RING][NH]
+    static constexpr int REF_OFF = QF_OFF + QF_RING * NH * 4;   // fp32 [NH]
+    static constexpr int FAC_OFF = REF_OFF + NH * 4;      // fp32 [NH]: rescale factors, then 1 / l
+    static constexpr int RED_OFF = FAC_OFF + NH * 4;      // fp32 [8][32]
+    static constexpr int VALID_OFF = RED_OFF + 1024;      // uint32 [VALID_RING][4]
+    static constexpr int BAR_OFF = VALID_OFF + VALID_RING * 16;
+    static constexpr int B_QFULL = 0, B_QFREE = 1, B_UFULL = 2, B_UFREE = B_UFULL + MAX_RING,
+                         B_SFULL = B_UFREE + MAX_RING, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
+                         B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1, NBARS = B_OFREE + 1;
+    static constexpr int START_OFF = BAR_OFF + NBARS * 8; // int64 first offset, count; int pair
+    static constexpr int TADDR_OFF = START_OFF + 24;
+    static constexpr int ABORT_OFF = TADDR_OFF + 4;
+    static constexpr int BYTES = ABORT_OFF + 4;
+    static_assert(BYTES <= 227 * 1024, "shared memory budget");
+    // TMEM: O^T unit u at columns u NH, S buffer i at (U + i) NH
+    static constexpr uint32_t COLS_USED = (U + 2) * NH;
+    static constexpr uint32_t COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
+    static_assert(COLS_USED <= 512, "tensor memory");
+};
+
+static __device__ int g_paged_attn_error = 0;
+
+static __device__ __forceinline__ void raise_abort(volatile int *abort) {
+    *abort = 1;
+    atomicExch(&g_paged_attn_error, 1);
+}
+// Wait for a phase, suspended in try_wait; false at once when the CTA has
+// aborted, or, raising the abort, when WAIT_NS pass.
+static __device__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (test_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; it++) {
+        if (try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if ((it & 15) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > WAIT_NS) {
+                raise_abort(abort);
+                return false;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- tensor memory
+// N columns (8, 16 or 32) of a warp's 32 lanes, thread t its lane t.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t ta, float (&v)[N]) {
+    if constexpr (N == 32) {
+        tmem_ld_32x32b_32(ta, v);
+    } else if constexpr (N == 16) {
+        tmem_ld_32x32b_16(ta, v);
+    } else {
+        static_assert(N == 8, "columns");
+        uint32_t r[8];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(ta)
+                     : "memory");
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                     :
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t ta, const float (&v)[N]) {
+    if constexpr (N == 32) {
+        tmem_st_32x32b_32(ta, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta + i),
+                         "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), "r"(__float_as_uint(v[i + 2])),
+                         "r"(__float_as_uint(v[i + 3])), "r"(__float_as_uint(v[i + 4])),
+                         "r"(__float_as_uint(v[i + 5])), "r"(__float_as_uint(v[i + 6])),
+                         "r"(__float_as_uint(v[i + 7]))
+                         : "memory");
+    }
+}
+
+// Sums of N values over the warp's lanes: lane i (mod N) receives that of value i.
+template <int N>
+__device__ __forceinline__ float columns_sum(float (&x)[N], int lane) {
+#pragma unroll
+    for (int w = N / 2; w >= 1; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; i++) {
+            const float send = up ? x[i] : x[i + w], keep = up ? x[i + w] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+        }
+    }
+#pragma unroll
+    for (int b = N; b < 32; b <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], b);
+    return x[0];
+}
+
+// Maximum of x over the warp (NaN counts as -inf).
+__device__ __forceinline__ float warp_max(float x) {
+    const int b = x != x ? (int)0xFF800000 : __float_as_int(x);
+    const int k = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7FFFFFFF);
+    return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
+}
+
+// ---------------------------------------------------------------- rows to 16-bit values
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(0x80008000u));
+    return r;
+}
+// Eight codes -> four pairs of f16 values of E2M1.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n.reg .b8 b0, b1, b2, b3;\nmov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\ncvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\ncvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+// f16 rows: eight codes times an E4M3 scale (splat in s).
+__device__ __forceinline__ uint4 rows_f16(uint32_t w, uint32_t s) {
+    uint32_t h[4];
+    e2m1x8_to_f16(w, h);
+    return make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));
+}
+// bf16 rows: eight codes times 2^(E - 127). The f16 bits of an E2M1 value moved
+// down by three are the bf16 value times 2^-112 (all its mantissa bits are zero
+// but the top one), so one product with 2^(E - 15) ends it; a scale above
+// 2^15, where that factor leaves bf16's range, takes a second one.
+struct MxScale {
+    uint32_t first, second;
+};
+__device__ __forceinline__ MxScale mx_scale(uint32_t E) {
+    // 2^(E - 15) as bf16, from the exponent field E + 112 (E <= 142)
+    const uint32_t e1 = E < 142u ? E : 142u;
+    const uint32_t f = (e1 + 112u) << 7, s = (E - e1 + 127u) << 7;
+    MxScale m{f | f << 16, s | s << 16};
+    if (E == 255u) m.second = 0x7FC07FC0u;  // NaN
+    return m;
+}
+__device__ __forceinline__ uint4 rows_bf16(uint32_t w, MxScale s) {
+    uint32_t h[4];
+    e2m1x8_to_f16(w, h);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        h[i] = ((h[i] >> 3) & 0x0FFF0FFFu) | (h[i] & 0x80008000u);
+        h[i] = mul_bf16x2(h[i], s.first);
+        if (s.second != 0x3F803F80u) h[i] = mul_bf16x2(h[i], s.second);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Where a CTA stands in the list of tiles.
+struct Walk {
+    int b, g;        // sequence and head group
+    int64_t tile;    // of the sequence
+    Seq s;
+    // to the next tile; the caller never walks past its last
+    __device__ __forceinline__ void next(const Args &a, bool more) {
+        if (++tile < s.tiles || !more) return;
+        tile = 0;
+        if (++g < a.groups) return;
+        g = 0;
+        do {
+            s = seq_of(a, ++b);
+        } while (s.tiles == 0);
+    }
+    // position of key r of this tile, -1 if there is none
+    __device__ __forceinline__ int64_t position(int r) const {
+        const int64_t j = tile * TK + r;
+        return j >= s.nvis ? -1 : j < s.ns ? j : s.w0 + j - s.ns;
+    }
+    // keys of this tile, rounded up to the 16 of an MMA step
+    __device__ __forceinline__ int keys16() const {
+        const int64_t k = s.nvis - tile * TK;
+        return k >= TK ? TK : ((int)k + 15) & ~15;
+    }
+};
+
+// Byte offset of 16-byte piece p of key row k in a tile of weights with rows of
+// 2 NH bytes, in the swizzle of that width.
+template <int NH>
+__device__ __forceinline__ uint32_t p_offset(int k, int p) {
+    if constexpr (NH == 64) return sw128(k, p);
+    if constexpr (NH == 32) return (uint32_t)(k * 64 + ((p ^ ((k >> 1) & 3)) << 4));
+    return (uint32_t)(k * 32 + ((p ^ ((k >> 2) & 1)) << 4));
+}
+template <int NH>
+__device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
+    if constexpr (NH == 64) return sdesc_sw<2>(addr, 16, 1024);
+    if constexpr (NH == 32) return sdesc_sw<4>(addr, 16, 512);
+    return sdesc_sw<6>(addr, 16, 256);
+}
+
+// A position in a ring of N and the parity of its round.
+template <int N>
+struct Ring {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <bool MX, int U, int NH>
+__global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
+    using L = Layout<MX, U, NH>;
+    constexpr int NC = NH / 2;  // heads per softmax thread
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t base = smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + L::ABORT_OFF);
+    auto bar = [&](uint32_t i) { return base + L::BAR_OFF + 8u * i; };
+    const int G = gridDim.x, cta = blockIdx.x;
+    grid_dep_launch();
+
+    if (tid == 0) {
+        mbar_init(bar(L::B_QFULL), NLOAD / 32);
+        mbar_init(bar(L::B_QFREE), 1);
+        for (int i = 0; i < L::NU; i++) {
+            mbar_init(bar(L::B_UFULL + i), NLOAD / 32);
+            mbar_init(bar(L::B_UFREE + i), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(L::B_SFULL + i), 1);
+            mbar_init(bar(L::B_SFREE + i), NSOFT / 32);
+            mbar_init(bar(L::B_PFULL + i), NSOFT / 32);
+            mbar_init(bar(L::B_PFREE + i), 1);
+        }
+        mbar_init(bar(L::B_OFULL), 1);
+        mbar_init(bar(L::B_OFREE), NSOFT / 32);
+        *abort = (base & 1023u) != 0;  // the swizzles want this alignment
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == MMA_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
+
+    // ---- this CTA's share of the tiles: totals, then where its first tile lies
+    int64_t *red = reinterpret_cast<int64_t *>(sm + L::RED_OFF);  // [17], and the total at [31]
+    int64_t *start = reinterpret_cast<int64_t *>(sm + L::START_OFF);
+    int64_t total = 0;
+    for (int b = tid; b < a.B; b += THREADS) total += seq_of(a, b).tiles;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane == 0) red[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < THREADS / 32; w++) total += red[w];
+    const int64_t T = total * a.groups;
+    const int sharers = sharing(T, G);
+    const int64_t t_begin = cta < sharers ? share_begin(cta, T, sharers) : T;
+    const int64_t t_end = cta < sharers ? share_begin(cta + 1, T, sharers) : T;
+    {
+        int64_t before = 0;  // tiles of the sequences before this chunk
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            // CTA 0 writes every prefix, the others stop at their first tile
+            if (cta != 0 && (t_begin == t_end || before * a.groups > t_begin)) break;
+            const int b = b0 + tid;
+            const int64_t v = b < a.B ? seq_of(a, b).tiles : 0;
+            int64_t x = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) red[warp] = x;
+            __syncthreads();
+            int64_t at = before + x - v;
+            for (int w = 0; w < THREADS / 32; w++) {
+                if (w < warp) at += red[w];
+                before += red[w];
+            }
+            if (cta == 0 && b < a.B) a.prefix[b] = at;
+            if (t_begin < t_end && at * a.groups <= t_begin && t_begin < (at + v) * a.groups) {
+                start[0] = (t_begin - at * a.groups) % v;
+                reinterpret_cast<int *>(start + 1)[0] = b;
+                reinterpret_cast<int *>(start + 1)[1] = (int)((t_begin - at * a.groups) / v);
+            }
+        }
+        if (cta == 0 && tid == 0) a.prefix[a.B] = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::TADDR_OFF);
+    const int64_t n_tiles = t_end - t_begin;
+    Walk w{};
+    if (n_tiles > 0) {
+        w.b = reinterpret_cast<int *>(start + 1)[0];
+        w.g = reinterpret_cast<int *>(start + 1)[1];
+        w.tile = start[0];
+        w.s = seq_of(a, w.b);
+    }
+
+    if (n_tiles == 0 || *abort) {
+        // nothing to do
+    } else if (warp < NSOFT / 32) {
+        // ------------------------------------------------ softmax and epilogue
+        const int quad = warp & 3, part = warp >> 2;  // lanes of TMEM, half of the heads
+        const int key = quad * 32 + lane, gt = tid & 127;
+        const int bar_id = 1 + part;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        float *ref = reinterpret_cast<float *>(sm + L::REF_OFF) + part * NC;
+        float *fac = reinterpret_cast<float *>(sm + L::FAC_OFF) + part * NC;
+        float *red_f = reinterpret_cast<float *>(sm + L::RED_OFF) + part * 128;  // [4][NC]
+        const volatile uint32_t *valid = reinterpret_cast<const volatile uint32_t *>(sm + L::VALID_OFF);
+        bool ok = true, first = true;
+        float l[NC];
+        uint32_t seg = 0;
+        Ring<2> sr;
+        Ring<L::NP> pr;
+        Ring<L::NU> ur;
+        for (int64_t k = 0; k < n_tiles; k++) {
+            if (first) {
+#pragma unroll
+                for (int i = 0; i < NC; i++) l[i] = 0.0f;
+            }
+            const float *qf = reinterpret_cast<const float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH + part * NC;
+            // the unit's barrier orders the load warps' writes of valid and qf
+            ok = wait_bar(bar(L::B_UFULL + ur.i), ur.phase, abort) && ok;
+            ok = wait_bar(bar(L::B_SFULL + sr.i), sr.phase, abort) && ok;
+            tc_fence_after();
+            float x[NC];
+            tmem_load<NC>(tmem + lanes + (U + sr.i) * NH + part * NC, x);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::B_SFREE + sr.i));
+            const bool see = ok && ((valid[(k % VALID_RING) * 4 + quad] >> lane) & 1);
+            float over = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NC; i++) {
+                x[i] = see ? x[i] * qf[i] : -INFINITY;
+                if (!first) over = fmaxf(over, x[i] - ref[i]);
+            }
+            const bool move = first || named_bar_or(bar_id, 128, over > RESCALE_LOG2);
+            if (move) {
+                float mine = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NC; i++) {
+                    const float m = warp_max(x[i]);
+                    if (lane == i) mine = m;
+                }
+                if (lane < NC) red_f[quad * NC + lane] = mine;
+                named_bar_sync(bar_id, 128);
+                if (gt < NC) {
+                    const float m = fmaxf(fmaxf(red_f[gt], red_f[NC + gt]), fmaxf(red_f[2 * NC + gt], red_f[3 * NC + gt]));
+                    const float old = ref[gt];
+                    const bool up = first || m > old + RESCALE_LOG2;
+                    const float now = up ? fmaxf(m, REF_NONE) : old;
+                    fac[gt] = first || !up ? 1.0f : ex2(old - now);
+                    ref[gt] = now;
+                }
+                named_bar_sync(bar_id, 128);
+            }
+            // this buffer's last P V is done, and with one buffer so is the last
+            // tile's; with two, a rescale waits for the other one too
+            ok = wait_bar(bar(L::B_PFREE + pr.i), pr.phase ^ 1, abort) && ok;
+            if (move && !first) {
+                if constexpr (L::NP == 2)
+                    ok = wait_bar(bar(L::B_PFREE + (pr.i ^ 1)), pr.i ? pr.phase : pr.phase ^ 1, abort) && ok;
+                tc_fence_after();
+#pragma unroll 1
+                for (int u = 0; u < U; u++) {
+                    const uint32_t ta = tmem + lanes + u * NH + part * NC;
+                    float o[NC];
+                    tmem_load<NC>(ta, o);
+#pragma unroll
+                    for (int i = 0; i < NC; i++) o[i] *= fac[i];
+                    tmem_store<NC>(ta, o);
+                }
+                tmem_st_wait();
+#pragma unroll
+                for (int i = 0; i < NC; i++) l[i] *= fac[i];
+            }
+#pragma unroll
+            for (int i = 0; i < NC; i++) {
+                x[i] = ex2(x[i] - ref[i] + P_OFFSET);
+                l[i] += x[i];
+            }
+            const uint32_t pb = base + L::P_OFF + pr.i * L::PARTS * L::P_PART;
+#pragma unroll
+            for (int p = 0; p < NC / 8; p++) {
+                const uint32_t off = p_offset<NH>(key, part * (NC / 8) + p);
+                uint32_t v[4];
+                if constexpr (MX) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float x0 = x[8 * p + 2 * i], x1 = x[8 * p + 2 * i + 1];
+                        v[i] = pack_bf16x2(x0, x1);
+                        r[i] = pack_bf16x2(x0 - bf16_lo(v[i]), x1 - bf16_hi(v[i]));
+                    }
+                    st_shared_v4(pb + L::P_PART + off, make_uint4(r[0], r[1], r[2], r[3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) v[i] = pack_f16x2(x[8 * p + 2 * i], x[8 * p + 2 * i + 1]);
+                }
+                st_shared_v4(pb + off, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::B_PFULL + pr.i));
+            sr.next();
+            pr.next();
+#pragma unroll
+            for (int u = 0; u < U; u++) ur.next();
+
+            const bool end_seq = w.tile + 1 == w.s.tiles, last = end_seq || k + 1 == n_tiles;
+            first = last;
+            if (last) {
+                // ---- the pair's part of this CTA is done
+                const bool from_start = w.tile <= k;  // its first tile is this CTA's too
+                const bool whole = from_start && end_seq;
+                const int64_t seg_tiles = from_start ? w.tile + 1 : k + 1;
+                const int slot = 2 * cta + (k + 1 - seg_tiles == 0 ? 0 : 1);
+                const float s = columns_sum<NC>(l, lane);
+                if (lane < NC) red_f[quad * NC + lane] = s;
+                named_bar_sync(bar_id, 128);
+                const int h0 = w.g * NH + part * NC;
+                if (gt < NC) {
+                    const float sum = red_f[gt] + red_f[NC + gt] + red_f[2 * NC + gt] + red_f[3 * NC + gt];
+                    fac[gt] = sum != 0.0f ? 1.0f / sum : 0.0f;
+                    if (!whole) {
+                        float *ml = a.part_ml + ((int64_t)slot * NH + part * NC + gt) * 2;
+                        ml[0] = ref[gt];
+                        ml[1] = sum;
+                    } else if (a.lse && h0 + gt < a.Hq) {
+                        a.lse[(int64_t)w.b * a.Hq + h0 + gt] =
+                            sum != 0.0f ? (ref[gt] - P_OFFSET + log2f(sum)) * LN2 : -INFINITY;
+                    }
+                }
+                named_bar_sync(bar_id, 128);
+                ok = wait_bar(bar(L::B_OFULL), seg & 1, abort) && ok;
+                tc_fence_after();
+#pragma unroll 1
+                for (int u = 0; u < U; u++) {
+                    float o[NC];
+                    tmem_load<NC>(tmem + lanes + u * NH + part * NC, o);
+                    const int c = 128 * u + key;
+                    if (c < a.C) {
+                        if (whole) {
+                            uint16_t *dst = a.out + ((int64_t)w.b * a.Hq + h0) * a.C + c;
+#pragma unroll
+                            for (int i = 0; i < NC; i++)
+                                if (h0 + i < a.Hq) {
+                                    const __nv_bfloat16 v = __float2bfloat16_rn(o[i] * fac[i]);
+                                    dst[(int64_t)i * a.C] = *reinterpret_cast<const uint16_t *>(&v);
+                                }
+                        } else {
+                            float *dst = a.part_o + ((int64_t)slot * NH + part * NC) * (128 * U) + c;
+#pragma unroll
+                            for (int i = 0; i < NC; i++) dst[i * (128 * U)] = o[i];
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_OFREE));
+                seg++;
+            }
+            w.next(a, k + 1 < n_tiles);
+        }
+    } else if (warp < MMA_WARP) {
+        // ------------------------------------------------ loads and dequantization
+        const int lw = warp - NSOFT / 32;
+        const int half = lw & 1, rg = lw >> 1, r = rg * 32 + lane;  // chunk of the unit, key row
+        bool ok = true;
+        uint32_t seg = 0;
+        Ring<L::NU> ur;
+        uint4 code[U][2];   // the tile ahead: 64 channels of each unit
+        uint32_t scl[U];
+        const int row_bytes = a.C / 2, sf_bytes = a.C / (MX ? 32 : 16);
+        auto load_unit = [&](int u, int64_t row) {
+            const int c0 = 128 * u + 64 * half;
+            code[u][0] = code[u][1] = make_uint4(0, 0, 0, 0);
+            scl[u] = 0;
+            if (row >= 0 && c0 < a.C) {
+                const uint8_t *p = a.fp4 + row * row_bytes + c0 / 2;
+                const uint8_t *s = a.sf + row * sf_bytes;
+                const bool two = c0 + 32 < a.C;
+                code[u][0] = __ldg(reinterpret_cast<const uint4 *>(p));
+                if (two) code[u][1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+                if constexpr (MX) {
+                    scl[u] = __ldg(s + c0 / 32);
+                    if (two) scl[u] |= (uint32_t)__ldg(s + c0 / 32 + 1) << 8;
+                } else {
+                    const uint16_t *s2 = reinterpret_cast<const uint16_t *>(s + c0 / 16);
+                    scl[u] = __ldg(s2);
+                    if (two) scl[u] |= (uint32_t)__ldg(s2 + 1) << 16;
+                }
+            }
+        };
+        // tile k + 1's row is looked up one tile before its loads are issued
+        int64_t row = paged_row(a.pk, w.b, w.position(r));
+        bool here = row >= 0;
+#pragma unroll
+        for (int u = 0; u < U; u++) load_unit(u, row);
+        Walk ahead = w;
+        int64_t row_next = -1;
+        if (n_tiles > 1) {
+            ahead.next(a, true);
+            row_next = paged_row(a.pk, ahead.b, ahead.position(r));
+        }
+        bool first = true;
+        for (int64_t k = 0; k < n_tiles; k++) {
+            if (first) {
+                // ---- queries of a new pair: one warp a head, lanes over channels
+                ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
+                float *qf = reinterpret_cast<float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH;
+                for (int h = lw; h < NH; h += NLOAD / 32) {
+                    const bool in = w.g * NH + h < a.Hq;
+                    const uint16_t *q = a.q + ((int64_t)w.b * a.Hq + w.g * NH + h) * a.C;
+                    uint4 v[(U + 1) / 2];
+                    uint32_t top = 0;  // largest |q| as bf16 bits (NaN and inf above all others)
+#pragma unroll
+                    for (int i = 0; i < (U + 1) / 2; i++) {
+                        const int c = 256 * i + 8 * lane;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (in && c < a.C) v[i] = __ldg(reinterpret_cast<const uint4 *>(q + c));
+                        const uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t lo = u4[j] & 0x7FFF, hi = (u4[j] >> 16) & 0x7FFF;
+                            top = max(top, max(lo, hi));
+                        }
+                    }
+                    float mul = 1.0f, f = a.scale * LOG2E;
+                    if constexpr (!MX) {
+                        top = __reduce_max_sync(0xffffffffu, top);
+                        // 2^e with the top exponent brought to 13; e <= 100 keeps 2^e in range
+                        int e = 13 - ((int)(top >> 7) - 127);
+                        e = e > 100 ? 100 : e;
+                        mul = __uint_as_float((uint32_t)(e + 127) << 23);
+                        f *= __uint_as_float((uint32_t)(127 - e) << 23);
+                    }
+                    if (lane == 0) qf[h] = f;
+#pragma unroll
+                    for (int i = 0; i < (U + 1) / 2; i++) {
+                        const int c = 256 * i + 8 * lane;
+                        if (c >= 128 * U) continue;
+                        uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        if constexpr (!MX) {
+#pragma unroll
+                            for (int j = 0; j < 4; j++) u4[j] = pack_f16x2(bf16_lo(u4[j]) * mul, bf16_hi(u4[j]) * mul);
+                        }
+                        st_shared_v4(base + L::Q_OFF + (c >> 6) * L::Q_CHUNK + sw128(h, (c >> 3) & 7),
+                                     make_uint4(u4[0], u4[1], u4[2], u4[3]));
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_QFULL));
+                seg++;
+            }
+            first = w.tile + 1 == w.s.tiles;
+            const uint32_t seen = __ballot_sync(0xffffffffu, here);
+            const bool write = r < w.keys16();
+            // rows of the tile after the next, while the next one's loads go out
+            const int64_t row_load = row_next;
+            if (k + 2 < n_tiles) {
+                ahead.next(a, true);
+                row_next = paged_row(a.pk, ahead.b, ahead.position(r));
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                ok = wait_bar(bar(L::B_UFREE + ur.i), ur.phase ^ 1, abort) && ok;
+                if (u == 0 && half == 0 && lane == 0)
+                    reinterpret_cast<volatile uint32_t *>(sm + L::VALID_OFF)[(k % VALID_RING) * 4 + rg] = seen;
+                if (write && 128 * u + 64 * half < a.C) {
+                    const uint32_t dst = base + L::K_OFF + ur.i * UNIT + half * CHUNK;
+                    const uint32_t wd[8] = {code[u][0].x, code[u][0].y, code[u][0].z, code[u][0].w,
+                                            code[u][1].x, code[u][1].y, code[u][1].z, code[u][1].w};
+                    if constexpr (MX) {
+                        const MxScale s0 = mx_scale(scl[u] & 0xFF), s1 = mx_scale((scl[u] >> 8) & 0xFF);
+#pragma unroll
+                        for (int p = 0; p < 8; p++) st_shared_v4(dst + sw128(r, p), rows_bf16(wd[p], p < 4 ? s0 : s1));
+                    } else {
+                        uint32_t s01, s23;  // two f16 scales each
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s01) : "h"((uint16_t)scl[u]));
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s23) : "h"((uint16_t)(scl[u] >> 16)));
+                        const uint32_t s[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                                               __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+#pragma unroll
+                        for (int p = 0; p < 8; p++) st_shared_v4(dst + sw128(r, p), rows_f16(wd[p], s[p >> 1]));
+                    }
+                }
+                if (k + 1 < n_tiles) load_unit(u, row_load);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_UFULL + ur.i));
+                ur.next();
+            }
+            here = row_load >= 0;
+            w.next(a, k + 1 < n_tiles);
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------ MMA issue
+        constexpr uint32_t id_s = MX ? idesc_bf16(128, NH, false) : idesc_f16(128, NH, false);
+        constexpr uint32_t id_o = MX ? idesc_bf16(128, NH, true, true) : idesc_f16(128, NH, true, true);
+        const uint64_t dq = sdesc(base + L::Q_OFF, 16, 1024);
+        const uint64_t dk = sdesc(base + L::K_OFF, 16, 1024);
+        const uint64_t dv = sdesc(base + L::K_OFF, CHUNK, 1024);
+        const uint64_t dp = p_desc<NH>(base + L::P_OFF);
+        Walk ws = w, wp = w;  // of S and of P V
+        int64_t ks = 0, kp = 0;
+        int us = 0;                      // next unit of S
+        bool s_first = true, p_first = true;
+        uint32_t s_seg = 0, p_seg = 0;
+        Ring<2> sr;
+        Ring<L::NP> pr;
+        Ring<L::NU> su, pu;
+        uint64_t last_step = globaltimer_ns();
+        while (kp < n_tiles && !*abort) {
+            bool progressed = false;
+            const bool s_cand = ks < n_tiles && ks < kp + 2;
+            if (kp < ks) {
+                const bool ready = s_cand ? test_wait(bar(L::B_PFULL + pr.i), pr.phase)
+                                          : try_wait_hint(bar(L::B_PFULL + pr.i), pr.phase, 1000);
+                if (ready && (!p_first || test_wait(bar(L::B_OFREE), (p_seg & 1) ^ 1))) {
+                    tc_fence_after();
+                    const int steps = wp.keys16() / 16;
+                    const uint64_t p0 = dp + (uint64_t)((pr.i * L::PARTS * L::P_PART) >> 4);
+                    for (int u = 0; u < U; u++) {
+                        const uint64_t v0 = dv + (uint64_t)((pu.i * UNIT) >> 4);
+                        for (int s = 0; s < steps; s++) {
+                            const uint64_t vd = v0 + (uint64_t)((s * 2048) >> 4);
+                            const uint64_t pd = p0 + (uint64_t)((s * 16 * NH * 2) >> 4);
+                            mma_bf16(tmem + u * NH, vd, pd, id_o, !p_first || s > 0 ? 1u : 0u);
+                            if constexpr (MX) mma_bf16(tmem + u * NH, vd, pd + (uint64_t)(L::P_PART >> 4), id_o, 1u);
+                        }
+                        mma_commit(bar(L::B_UFREE + pu.i));
+                        pu.next();
+                    }
+                    mma_commit(bar(L::B_PFREE + pr.i));
+                    pr.next();
+                    p_first = wp.tile + 1 == wp.s.tiles;
+                    if (p_first || kp + 1 == n_tiles) {
+                        mma_commit(bar(L::B_OFULL));
+                        p_seg++;
+                    }
+                    kp++;
+                    wp.next(a, kp < n_tiles);
+                    progressed = true;
+                }
+            }
+            if (!progressed && s_cand) {
+                if ((us > 0 || ((!s_first || test_wait(bar(L::B_QFULL), s_seg & 1)) &&
+                                test_wait(bar(L::B_SFREE + sr.i), sr.phase ^ 1))) &&
+                    try_wait_hint(bar(L::B_UFULL + su.i), su.phase, kp < ks ? 200 : 1000)) {
+                    tc_fence_after();
+                    const uint64_t k0 = dk + (uint64_t)((su.i * UNIT) >> 4);
+                    const uint64_t q0 = dq + (uint64_t)((us * 2 * L::Q_CHUNK) >> 4);
+                    const uint32_t sd = tmem + (U + sr.i) * NH;
+                    const int left = (a.C - 128 * us) / 16, steps = left < 8 ? left : 8;
+                    for (int s = 0; s < steps; s++)
+                        mma_bf16(sd, k0 + (uint64_t)(((s >> 2) * CHUNK + (s & 3) * 32) >> 4),
+                                 q0 + (uint64_t)(((s >> 2) * L::Q_CHUNK + (s & 3) * 32) >> 4), id_s,
+                                 us > 0 || s > 0 ? 1u : 0u);
+                    su.next();
+                    if (++us == U) {
+                        us = 0;
+                        mma_commit(bar(L::B_SFULL + sr.i));
+                        sr.next();
+                        s_first = ws.tile + 1 == ws.s.tiles;
+                        if (s_first) {
+                            mma_commit(bar(L::B_QFREE));
+                            s_seg++;
+                        }
+                        ks++;
+                        ws.next(a, ks < n_tiles);
+                    }
+                    progressed = true;
+                }
+            }
+            if (progressed) {
+                last_step = globaltimer_ns();
+            } else if (globaltimer_ns() - last_step > WAIT_NS) {
+                raise_abort(abort);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) a.flags[cta] = *abort;
+    if (*abort) {
+        // MMAs still in flight land before the CTA's memory is released
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::COLS);
+    }
+}
+
+template <bool MX, int U, int NH>
+int launch_one(const Args &a, int G, cudaStream_t s) {
+    using L = Layout<MX, U, NH>;
+    static PerDevice smem_set;
+    if (!set_smem_limit_once(smem_set, attn_kernel<MX, U, NH>, L::BYTES)) return CSA2_ERR_CUDA;
+    return launch_kernel(false, attn_kernel<MX, U, NH>, dim3((unsigned)G), dim3(THREADS), L::BYTES, s, a);
+}
+
+// The kernel for C channels and head groups of nh.
+template <bool MX>
+int launch_attn(const Args &a, int nh, int G, cudaStream_t s) {
+    const int u = (a.C + 127) / 128;
+#define CSA2_PA(U_)                                       \
+    if (u == U_) {                                        \
+        if (nh == 16) return launch_one<MX, U_, 16>(a, G, s); \
+        if (nh == 32) return launch_one<MX, U_, 32>(a, G, s); \
+        return launch_one<MX, U_, 64>(a, G, s);           \
+    }
+    CSA2_PA(1)
+    CSA2_PA(2)
+    CSA2_PA(3)
+    CSA2_PA(4)
+#undef CSA2_PA
+    return CSA2_ERR_SHAPE;
+}
+
+int launch_paged_attn_fp4(const Args &a, int nh, int G, cudaStream_t s);
+int launch_paged_attn_mxfp4(const Args &a, int nh, int G, cudaStream_t s);
+
+}  // namespace pa
+}  // namespace csa2

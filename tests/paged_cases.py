@@ -39,7 +39,10 @@ def attend(q, fp4, sf, table, lens, scale, win=0, sink=0, mx=False):
     so it is off by at most C 2^-23 |scale| sum|q k| (any summation order, and
     accumulators that truncate); the weights then by a factor of 1 +- 2 d with d
     that bound, by 2^-11 for weights rounded to 16-bit floats, and by 2^-18 for
-    exp and the fp32 sums; the output once more by half a bf16 step, 2^-8."""
+    exp and the fp32 sums; the output once more by half a bf16 step, 2^-8. A
+    16-bit float of step 2^-24 rounds a small weight by up to 2^-25; the largest
+    weight is held at 2^7 or more, so that is 2^-32 of the weights' sum, for each
+    key: 2^-32 sum_j |v_j|, felt where a channel is zero in all keys that count."""
     B, H, C = q.shape
     n_pages, page = fp4.shape[:2]
     outs, lses, bounds, lse_bounds = [], [], [], []
@@ -67,7 +70,7 @@ def attend(q, fp4, sf, table, lens, scale, win=0, sink=0, mx=False):
         eps = 2 * d + 2.0 ** -11 + 2.0 ** -18
         outs.append(o)
         lses.append(lse)
-        bounds.append(2.0 ** -8 * o.abs() + (1 + 2.0 ** -8) * eps[:, None] * (p @ kv.abs()) + 1e-30)
+        bounds.append(2.0 ** -8 * o.abs() + (1 + 2.0 ** -8) * eps[:, None] * (p @ kv.abs()) + 2.0 ** -32 * kv.abs().sum(0) + 1e-30)
         lse_bounds.append(d + 2.0 ** -20 * (1 + lse.abs()))
     return torch.stack(outs), torch.stack(lses), torch.stack(bounds), torch.stack(lse_bounds)
 

@@ -132,6 +132,7 @@ def test_attention_refusals(B, mx):
         assert call(B, name, good, **change) == SHAPE, change
     assert call(B, name, good, win=-1) == RANGE and call(B, name, good, sink=-1) == RANGE
     assert call(B, name, good, q=ODD8) == ALIGN and call(B, name, good, fp4=ODD8) == ALIGN
+    assert call(B, name, good, out=ODD4) == ALIGN
     assert call(B, name, good, ws=None) == WS and call(B, name, good, wsb=need - 1) == WS
     assert call(B, name, good, ws=ODD8) == ALIGN
     assert call(B, name, good, B=0) == 0

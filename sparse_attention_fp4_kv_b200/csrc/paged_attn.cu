@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const Args a, int NH, int pitc
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
             out[tid] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         }
-        if (tid == 0 && lse) *lse = sum != 0.0f ? (m - P_OFFSET + log2f(sum)) * LN2 : -INFINITY;
+        if (tid == 0 && lse) *lse = sum != 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
         __syncthreads();
     }
 }
@@ -145,6 +145,8 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
     if (B < 0 || Hq < 1 || Hq > 256 || C < 32 || C > 512 || C % 32 ||
         !paged_shape_ok(max_pages, page_size, n_pages))
         return CSA2_ERR_SHAPE;
+    const int64_t cap = (int64_t)max_pages * page_size;
+    if (cap > INT32_MAX) return CSA2_ERR_SHAPE;
     if (n_win < 0 || n_sink < 0) return CSA2_ERR_RANGE;
     if (!aligned(q, 16) || !aligned(fp4, 16) || !aligned(out, 8) || (!mx && !aligned(sf, 4))) return CSA2_ERR_ALIGN;
     if (B == 0) return CSA2_OK;
@@ -154,8 +156,9 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
     if (!ws || ws_bytes < w.bytes) return CSA2_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return CSA2_ERR_ALIGN;
     cudaStream_t s = (cudaStream_t)stream;
-    const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len, n_win,
-                 n_sink, B, Hq, C, groups, scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
+    const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len,
+                 (int)(n_win < cap ? n_win : cap), (int)(n_sink < cap ? n_sink : cap), (int)cap, B, Hq, C, groups,
+                 C % 128 == 0 && aligned(sf, mx ? 4 : 8), scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
     const int st = mx ? launch_paged_attn_mxfp4(a, nh, G, s) : launch_paged_attn_fp4(a, nh, G, s);
     if (st != CSA2_OK) return st;
     // one head per block until there are a few blocks per SM

@@ -1,8 +1,8 @@
 // Attention of one new token over a paged FP4 cache: the tensor-core kernel.
 // paged_attn.cu and paged_attn_mx.cu instantiate it for the two scale formats.
 //
-//   S^T[key, head]  = K Q^T        M = 128 keys, N = heads, K = channels
-//   O^T[chan, head] += V^T P^T     M = 128 channels, N = heads, K = 128 keys
+//   S^T[key, head]  = K Q^T        M = 64 keys, N = heads, K = channels
+//   O^T[chan, head] += V^T P^T     M = 128 channels, N = heads, K = 64 keys
 // with K = V = the dequantized rows. Keys and channels lie on the MMAs' 128 rows
 // because a decode query has 64 heads or fewer, and M = 64 runs at half rate.
 //
@@ -53,25 +53,27 @@ struct Args {
     const uint8_t *fp4, *sf;
     PagedKv pk;
     const int64_t *ctx_len;
-    int64_t win, sink;
+    int win, sink;         // 0: every position
+    int cap;               // max_pages * page_size
     int B, Hq, C, groups;  // groups of NH heads
+    bool wide_scales;      // a unit's scales of a row start on their size
     float scale;
     uint16_t *out;
     float *lse;
     // workspace
     int *flags;        // [G] a CTA that gave up a wait
     int64_t *prefix;   // [B + 1] tiles before sequence b
-    float *part_ml;    // [2 G][NH][2]
+    float *part_ml;    // [2 G][NH][2]: reference - P_OFFSET, sum
     float *part_o;     // [2 G][NH][128 U]
 };
 
-constexpr int TK = 128;             // keys per tile
+constexpr int TK = 64;              // keys per tile
 constexpr int CHUNK = TK * 128;     // 64 channels of a tile: rows of 128 bytes
 constexpr int UNIT = 2 * CHUNK;
 constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 32;
 constexpr int MMA_WARP = (NSOFT + NLOAD) / 32;
-constexpr int MAX_RING = 6;
-constexpr int VALID_RING = 8, QF_RING = 4;
+constexpr int MAX_RING = 8;          // tiles of the ring, and steps
+constexpr int VALID_RING = 16, QF_RING = 3;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.0f;  // how far a score may exceed the reference
 constexpr float P_OFFSET = 7.0f;      // weights are 2^(x - r + 7) <= 2^15
@@ -81,12 +83,11 @@ constexpr uint64_t WAIT_NS = 200ull * 1000 * 1000;
 // Visible keys of a sequence of n tokens: positions [0, ns) and [w0, n), listed
 // in that order.
 struct Seq {
-    int64_t nvis, ns, w0, tiles;
+    int nvis, ns, w0, tiles;
 };
 __device__ __forceinline__ Seq seq_of(const Args &a, int b) {
-    int64_t n = __ldg(a.ctx_len + b);
-    const int64_t cap = (int64_t)a.pk.max_pages * a.pk.page_size;
-    n = n > cap ? cap : n < 0 ? 0 : n;
+    const int64_t len = __ldg(a.ctx_len + b);
+    const int n = len > a.cap ? a.cap : len < 0 ? 0 : (int)len;
     Seq s;
     s.ns = s.w0 = 0;
     if (a.win > 0) {
@@ -94,7 +95,7 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b) {
         s.w0 = n - a.win > s.ns ? n - a.win : s.ns;
     }
     s.nvis = s.ns + n - s.w0;
-    s.tiles = (s.nvis + TK - 1) / TK;
+    s.tiles = (int)(((uint32_t)s.nvis + TK - 1) / TK);
     return s;
 }
 
@@ -107,22 +108,24 @@ __device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (i
 template <bool MX, int U, int NH>
 struct Layout {
     static constexpr int PARTS = MX ? 2 : 1;       // of the weights
-    static constexpr int NP = (U == 4 && NH == 64) ? 1 : 2;  // buffers of weights
+    static constexpr int NP = 2;                   // buffers of weights
     static constexpr int P_PART = TK * NH * 2;
     static constexpr int Q_CHUNK = NH * 128;       // 64 channels of Q
     static constexpr int Q_OFF = 0;
     static constexpr int P_OFF = Q_OFF + 2 * U * Q_CHUNK;
     static constexpr int K_OFF = P_OFF + NP * PARTS * P_PART;
     static constexpr int SMALL = 3072;
-    static constexpr int FIT = (227 * 1024 - SMALL - K_OFF) / UNIT;
-    static constexpr int NU = FIT < MAX_RING ? FIT : MAX_RING;  // units of the ring
-    static_assert(NU >= U, "a tile fits the ring");
-    static constexpr int QF_OFF = K_OFF + NU * UNIT;      // fp32 [QF_RING][NH]
-    static constexpr int REF_OFF = QF_OFF + QF_RING * NH * 4;   // fp32 [NH]
+    static constexpr int FIT = (227 * 1024 - SMALL - K_OFF) / (U * UNIT);
+    static constexpr int NS = (U + 1) / 2;                 // steps of a tile: two units each, the last maybe one
+    static constexpr int NT = FIT * NS < MAX_RING ? FIT : MAX_RING / NS;  // tiles of the ring
+    static_assert(NT >= 2, "two tiles fit the ring: P V of one beside S of the next");
+    static constexpr int QF_OFF = K_OFF + NT * U * UNIT;      // fp32 [QF_RING][NH]
+    static constexpr int REF_OFF = QF_OFF + QF_RING * NH * 4;   // fp32 [NH]: P_OFFSET - reference
     static constexpr int FAC_OFF = REF_OFF + NH * 4;      // fp32 [NH]: rescale factors, then 1 / l
     static constexpr int RED_OFF = FAC_OFF + NH * 4;      // fp32 [8][32]
-    static constexpr int VALID_OFF = RED_OFF + 1024;      // uint32 [VALID_RING][4]
-    static constexpr int BAR_OFF = VALID_OFF + VALID_RING * 16;
+    static constexpr int VALID_OFF = RED_OFF + 1024;      // a bit per key, 64 bits [VALID_RING]
+    static constexpr int INFO_OFF = VALID_OFF + VALID_RING * 8;  // int4 [VALID_RING]
+    static constexpr int BAR_OFF = INFO_OFF + VALID_RING * 16;
     static constexpr int B_QFULL = 0, B_QFREE = 1, B_UFULL = 2, B_UFREE = B_UFULL + MAX_RING,
                          B_SFULL = B_UFREE + MAX_RING, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
                          B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1, NBARS = B_OFREE + 1;
@@ -131,8 +134,9 @@ struct Layout {
     static constexpr int ABORT_OFF = TADDR_OFF + 4;
     static constexpr int BYTES = ABORT_OFF + 4;
     static_assert(BYTES <= 227 * 1024, "shared memory budget");
-    // TMEM: O^T unit u at columns u NH, S buffer i at (U + i) NH
-    static constexpr uint32_t COLS_USED = (U + 2) * NH;
+    // TMEM: O^T unit u at columns u NH; S at U NH, a 64-row result fills 16 lanes of
+    // each quadrant, buffer i those from 16 i on
+    static constexpr uint32_t COLS_USED = (U + 1) * NH;
     static constexpr uint32_t COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
     static_assert(COLS_USED <= 512, "tensor memory");
 };
@@ -151,7 +155,7 @@ static __device__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abo
     for (uint32_t it = 0;; it++) {
         if (try_wait(bar, parity)) return true;
         if (*abort) return false;
-        if ((it & 15) == 0) {
+        if ((it & 63) == 63) {  // reading the timer takes as long as a short wait
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) {
                 t0 = now;
@@ -186,6 +190,37 @@ __device__ __forceinline__ void tmem_load(uint32_t ta, float (&v)[N]) {
         for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
     }
 }
+// N columns (4, 8 or 16) of 16 lanes: threads 0-15 read columns [0, N), threads
+// 16-31 columns [N, 2 N).
+template <int N>
+__device__ __forceinline__ void tmem_load_half(uint32_t ta, float (&v)[N]) {
+    uint32_t r[N];
+    if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+            "%12, %13, %14, %15}, [%16], 16;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(ta));
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(ta));
+    } else {
+        static_assert(N == 4, "columns");
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0, %1, %2, %3}, [%4], 4;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(ta));
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+                     :
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = __uint_as_float(r[i]);
+}
 template <int N>
 __device__ __forceinline__ void tmem_store(uint32_t ta, const float (&v)[N]) {
     if constexpr (N == 32) {
@@ -202,7 +237,8 @@ __device__ __forceinline__ void tmem_store(uint32_t ta, const float (&v)[N]) {
     }
 }
 
-// Sums of N values over the warp's lanes: lane i (mod N) receives that of value i.
+// Sums of N <= 16 values over each half of the warp: lane i (mod N) of a half
+// receives that of value i.
 template <int N>
 __device__ __forceinline__ float columns_sum(float (&x)[N], int lane) {
 #pragma unroll
@@ -215,15 +251,31 @@ __device__ __forceinline__ float columns_sum(float (&x)[N], int lane) {
         }
     }
 #pragma unroll
-    for (int b = N; b < 32; b <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], b);
+    for (int b = N; b < 16; b <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], b);
     return x[0];
 }
+// The same for the maximum; NaN counts as -inf.
+template <int N>
+__device__ __forceinline__ float columns_max(float (&x)[N], int lane) {
+#pragma unroll
+    for (int w = N / 2; w >= 1; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; i++) {
+            const float send = up ? x[i] : x[i + w], keep = up ? x[i + w] : x[i];
+            x[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, w));
+        }
+    }
+#pragma unroll
+    for (int b = N; b < 16; b <<= 1) x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], b));
+    return x[0] == x[0] ? x[0] : -INFINITY;
+}
 
-// Maximum of x over the warp (NaN counts as -inf).
-__device__ __forceinline__ float warp_max(float x) {
-    const int b = x != x ? (int)0xFF800000 : __float_as_int(x);
-    const int k = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7FFFFFFF);
-    return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
+// True in one lane of a warp that is together, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
 }
 
 // ---------------------------------------------------------------- rows to 16-bit values
@@ -286,7 +338,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Where a CTA stands in the list of tiles.
 struct Walk {
     int b, g;        // sequence and head group
-    int64_t tile;    // of the sequence
+    int tile;        // of the sequence
     Seq s;
     // to the next tile; the caller never walks past its last
     __device__ __forceinline__ void next(const Args &a, bool more) {
@@ -299,14 +351,14 @@ struct Walk {
         } while (s.tiles == 0);
     }
     // position of key r of this tile, -1 if there is none
-    __device__ __forceinline__ int64_t position(int r) const {
-        const int64_t j = tile * TK + r;
-        return j >= s.nvis ? -1 : j < s.ns ? j : s.w0 + j - s.ns;
+    __device__ __forceinline__ int position(int r) const {
+        const int64_t j = (int64_t)tile * TK + r;
+        return j >= s.nvis ? -1 : (int)(j < s.ns ? j : s.w0 + j - s.ns);
     }
     // keys of this tile, rounded up to the 16 of an MMA step
     __device__ __forceinline__ int keys16() const {
-        const int64_t k = s.nvis - tile * TK;
-        return k >= TK ? TK : ((int)k + 15) & ~15;
+        const int k = s.nvis - tile * TK;
+        return k >= TK ? TK : (k + 15) & ~15;
     }
 };
 
@@ -325,6 +377,23 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
     return sdesc_sw<6>(addr, 16, 256);
 }
 
+// What the load warps tell the other roles about a tile, beside its keys.
+struct TileInfo {
+    int b, g;   // sequence and head group
+    int flags;  // kLast, kWhole, and the 16-key steps of P V
+    int slot;   // where this CTA's part of the pair goes
+};
+constexpr int kLast = 1;   // the CTA's last tile of the pair
+constexpr int kWhole = 2;  // the CTA has all tiles of the pair
+__device__ __forceinline__ TileInfo read_info(uint32_t info, uint32_t i) {
+    TileInfo v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.b), "=r"(v.g), "=r"(v.flags), "=r"(v.slot)
+                 : "r"(info + 16 * i)
+                 : "memory");
+    return v;
+}
+
 // A position in a ring of N and the parity of its round.
 template <int N>
 struct Ring {
@@ -340,7 +409,9 @@ struct Ring {
 template <bool MX, int U, int NH>
 __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     using L = Layout<MX, U, NH>;
-    constexpr int NC = NH / 2;  // heads per softmax thread
+    constexpr int NG = NH / 2;            // heads of a group of four softmax warps
+    constexpr int NC = NH / 4;            // heads per softmax thread
+    constexpr int W = NG < 16 ? NG : 16;  // columns of O^T in registers at a time
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -352,8 +423,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     if (tid == 0) {
         mbar_init(bar(L::B_QFULL), NLOAD / 32);
         mbar_init(bar(L::B_QFREE), 1);
-        for (int i = 0; i < L::NU; i++) {
-            mbar_init(bar(L::B_UFULL + i), NLOAD / 32);
+        for (int i = 0; i < L::NT * L::NS; i++) {
+            mbar_init(bar(L::B_UFULL + i), NLOAD / 32);  // step s of ring tile t: t NS + s
             mbar_init(bar(L::B_UFREE + i), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -418,12 +489,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::TADDR_OFF);
-    const int64_t n_tiles = t_end - t_begin;
+    const int n_tiles = (int)(t_end - t_begin);
     Walk w{};
     if (n_tiles > 0) {
         w.b = reinterpret_cast<int *>(start + 1)[0];
         w.g = reinterpret_cast<int *>(start + 1)[1];
-        w.tile = start[0];
+        w.tile = (int)start[0];
         w.s = seq_of(a, w.b);
     }
 
@@ -432,105 +503,140 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     } else if (warp < NSOFT / 32) {
         // ------------------------------------------------ softmax and epilogue
         const int quad = warp & 3, part = warp >> 2;  // lanes of TMEM, half of the heads
-        const int key = quad * 32 + lane, gt = tid & 127;
+        const int key = quad * 16 + (lane & 15), hq = lane >> 4;  // a thread: a key, a quarter of the heads
+        const int gt = tid & 127;
         const int bar_id = 1 + part;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        float *ref = reinterpret_cast<float *>(sm + L::REF_OFF) + part * NC;
-        float *fac = reinterpret_cast<float *>(sm + L::FAC_OFF) + part * NC;
-        float *red_f = reinterpret_cast<float *>(sm + L::RED_OFF) + part * 128;  // [4][NC]
-        const volatile uint32_t *valid = reinterpret_cast<const volatile uint32_t *>(sm + L::VALID_OFF);
+        // of this half of the heads
+        float *ref = reinterpret_cast<float *>(sm + L::REF_OFF) + part * NG;
+        float *fac = reinterpret_cast<float *>(sm + L::FAC_OFF) + part * NG;
+        float *red_f = reinterpret_cast<float *>(sm + L::RED_OFF) + part * 128;  // [4][NG]
+        const volatile uint16_t *valid = reinterpret_cast<const volatile uint16_t *>(sm + L::VALID_OFF);
         bool ok = true, first = true;
         float l[NC];
         uint32_t seg = 0;
-        Ring<2> sr;
-        Ring<L::NP> pr;
-        Ring<L::NU> ur;
-        for (int64_t k = 0; k < n_tiles; k++) {
+        Ring<2> sr, pr;
+        Ring<L::NT> ur;
+        for (int k = 0; k < n_tiles; k++) {
             if (first) {
 #pragma unroll
                 for (int i = 0; i < NC; i++) l[i] = 0.0f;
             }
-            const float *qf = reinterpret_cast<const float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH + part * NC;
-            // the unit's barrier orders the load warps' writes of valid and qf
-            ok = wait_bar(bar(L::B_UFULL + ur.i), ur.phase, abort) && ok;
+            const float *qf = reinterpret_cast<const float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH + part * NG + hq * NC;
+            const float *rq = ref + hq * NC;
+            // the step's barrier orders the load warps' writes of valid, info and qf
+            ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS), ur.phase, abort) && ok;
+            const uint32_t vi = (uint32_t)k % VALID_RING;
+            const TileInfo info = read_info(base + L::INFO_OFF, vi);
+            const uint32_t seen = ok ? valid[vi * 4 + quad] : 0u;
+            const bool see = (seen >> (lane & 15)) & 1;
+            float f[NC];
+#pragma unroll
+            for (int i = 0; i < NC; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(qf + i);
+                f[i] = v.x;
+                f[i + 1] = v.y;
+                f[i + 2] = v.z;
+                f[i + 3] = v.w;
+            }
             ok = wait_bar(bar(L::B_SFULL + sr.i), sr.phase, abort) && ok;
             tc_fence_after();
             float x[NC];
-            tmem_load<NC>(tmem + lanes + (U + sr.i) * NH + part * NC, x);
+            tmem_load_half<NC>(tmem + lanes + ((16u * sr.i) << 16) + U * NH + part * NG, x);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::B_SFREE + sr.i));
-            const bool see = ok && ((valid[(k % VALID_RING) * 4 + quad] >> lane) & 1);
-            float over = -INFINITY;
+            // ---- does a score exceed its head's reference by 2^8?
+            bool move = first;
+            if (!first) {
+                float over = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < NC; i++) {
-                x[i] = see ? x[i] * qf[i] : -INFINITY;
-                if (!first) over = fmaxf(over, x[i] - ref[i]);
-            }
-            const bool move = first || named_bar_or(bar_id, 128, over > RESCALE_LOG2);
-            if (move) {
-                float mine = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < NC; i++) {
-                    const float m = warp_max(x[i]);
-                    if (lane == i) mine = m;
+                for (int i = 0; i < NC; i += 4) {
+                    const float4 r = *reinterpret_cast<const float4 *>(rq + i);
+                    over = fmaxf(over, fmaxf(fmaf(x[i], f[i], r.x), fmaf(x[i + 1], f[i + 1], r.y)));
+                    over = fmaxf(over, fmaxf(fmaf(x[i + 2], f[i + 2], r.z), fmaf(x[i + 3], f[i + 3], r.w)));
                 }
-                if (lane < NC) red_f[quad * NC + lane] = mine;
+                move = named_bar_or(bar_id, 128, see && over > RESCALE_LOG2 + P_OFFSET);
+            }
+            if (move) {
+                float y[NC];
+#pragma unroll
+                for (int i = 0; i < NC; i++) y[i] = see ? x[i] * f[i] : -INFINITY;
+                const float mine = columns_max<NC>(y, lane);
+                if ((lane & 15) < NC) red_f[quad * NG + hq * NC + (lane & 15)] = mine;
                 named_bar_sync(bar_id, 128);
-                if (gt < NC) {
-                    const float m = fmaxf(fmaxf(red_f[gt], red_f[NC + gt]), fmaxf(red_f[2 * NC + gt], red_f[3 * NC + gt]));
-                    const float old = ref[gt];
+                if (gt < NG) {
+                    const float m = fmaxf(fmaxf(red_f[gt], red_f[NG + gt]), fmaxf(red_f[2 * NG + gt], red_f[3 * NG + gt]));
+                    const float old = P_OFFSET - ref[gt];
                     const bool up = first || m > old + RESCALE_LOG2;
                     const float now = up ? fmaxf(m, REF_NONE) : old;
                     fac[gt] = first || !up ? 1.0f : ex2(old - now);
-                    ref[gt] = now;
+                    if (up) ref[gt] = P_OFFSET - now;
                 }
                 named_bar_sync(bar_id, 128);
             }
-            // this buffer's last P V is done, and with one buffer so is the last
-            // tile's; with two, a rescale waits for the other one too
+            // this buffer's last P V is done; a rescale waits for the other one's too
             ok = wait_bar(bar(L::B_PFREE + pr.i), pr.phase ^ 1, abort) && ok;
             if (move && !first) {
-                if constexpr (L::NP == 2)
-                    ok = wait_bar(bar(L::B_PFREE + (pr.i ^ 1)), pr.i ? pr.phase : pr.phase ^ 1, abort) && ok;
+                ok = wait_bar(bar(L::B_PFREE + (pr.i ^ 1)), pr.i ? pr.phase : pr.phase ^ 1, abort) && ok;
                 tc_fence_after();
 #pragma unroll 1
-                for (int u = 0; u < U; u++) {
-                    const uint32_t ta = tmem + lanes + u * NH + part * NC;
-                    float o[NC];
-                    tmem_load<NC>(ta, o);
+                for (int u = 0; u < U; u++)
+#pragma unroll 1
+                    for (int c = 0; c < NG; c += W) {
+                        const uint32_t ta = tmem + lanes + u * NH + part * NG + c;
+                        float o[W];
+                        tmem_load<W>(ta, o);
 #pragma unroll
-                    for (int i = 0; i < NC; i++) o[i] *= fac[i];
-                    tmem_store<NC>(ta, o);
-                }
+                        for (int i = 0; i < W; i++) o[i] *= fac[c + i];
+                        tmem_store<W>(ta, o);
+                    }
                 tmem_st_wait();
 #pragma unroll
-                for (int i = 0; i < NC; i++) l[i] *= fac[i];
-            }
-#pragma unroll
-            for (int i = 0; i < NC; i++) {
-                x[i] = ex2(x[i] - ref[i] + P_OFFSET);
-                l[i] += x[i];
+                for (int i = 0; i < NC; i++) l[i] *= fac[hq * NC + i];
             }
             const uint32_t pb = base + L::P_OFF + pr.i * L::PARTS * L::P_PART;
 #pragma unroll
-            for (int p = 0; p < NC / 8; p++) {
-                const uint32_t off = p_offset<NH>(key, part * (NC / 8) + p);
-                uint32_t v[4];
+            for (int i = 0; i < NC; i += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(rq + i);
+                x[i] = ex2(fmaf(x[i], f[i], r.x));
+                x[i + 1] = ex2(fmaf(x[i + 1], f[i + 1], r.y));
+                x[i + 2] = ex2(fmaf(x[i + 2], f[i + 2], r.z));
+                x[i + 3] = ex2(fmaf(x[i + 3], f[i + 3], r.w));
+            }
+            if (!see) {  // a row without a key may hold anything
+#pragma unroll
+                for (int i = 0; i < NC; i++) x[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < NC; i++) l[i] += x[i];
+            uint32_t v[NC / 2], v2[NC / 2];  // weights, and (MX) what their rounding leaves
+#pragma unroll
+            for (int i = 0; i < NC / 2; i++) {
                 if constexpr (MX) {
-                    uint32_t r[4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float x0 = x[8 * p + 2 * i], x1 = x[8 * p + 2 * i + 1];
-                        v[i] = pack_bf16x2(x0, x1);
-                        r[i] = pack_bf16x2(x0 - bf16_lo(v[i]), x1 - bf16_hi(v[i]));
-                    }
-                    st_shared_v4(pb + L::P_PART + off, make_uint4(r[0], r[1], r[2], r[3]));
+                    v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                    v2[i] = pack_bf16x2(x[2 * i] - bf16_lo(v[i]), x[2 * i + 1] - bf16_hi(v[i]));
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) v[i] = pack_f16x2(x[8 * p + 2 * i], x[8 * p + 2 * i + 1]);
+                    v[i] = pack_f16x2(x[2 * i], x[2 * i + 1]);
                 }
-                st_shared_v4(pb + off, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+            // the thread's heads of its key's row: 2 NC bytes
+            const int byte0 = (part * NG + hq * NC) * 2;
+            if constexpr (NC >= 8) {
+#pragma unroll
+                for (int p = 0; p < NC / 8; p++) {
+                    const uint32_t off = p_offset<NH>(key, byte0 / 16 + p);
+                    st_shared_v4(pb + off, make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]));
+                    if constexpr (MX)
+                        st_shared_v4(pb + L::P_PART + off,
+                                     make_uint4(v2[4 * p], v2[4 * p + 1], v2[4 * p + 2], v2[4 * p + 3]));
+                }
+            } else {
+                const uint32_t off = p_offset<NH>(key, byte0 / 16) + byte0 % 16;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(pb + off), "r"(v[0]), "r"(v[1]) : "memory");
+                if constexpr (MX)
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(pb + L::P_PART + off), "r"(v2[0]), "r"(v2[1])
+                                 : "memory");
             }
             fence_proxy_async();
             tc_fence_before();
@@ -538,31 +644,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             if (lane == 0) mbar_arrive(bar(L::B_PFULL + pr.i));
             sr.next();
             pr.next();
-#pragma unroll
-            for (int u = 0; u < U; u++) ur.next();
+            ur.next();
 
-            const bool end_seq = w.tile + 1 == w.s.tiles, last = end_seq || k + 1 == n_tiles;
-            first = last;
-            if (last) {
+            first = info.flags & kLast;
+            if (first) {
                 // ---- the pair's part of this CTA is done
-                const bool from_start = w.tile <= k;  // its first tile is this CTA's too
-                const bool whole = from_start && end_seq;
-                const int64_t seg_tiles = from_start ? w.tile + 1 : k + 1;
-                const int slot = 2 * cta + (k + 1 - seg_tiles == 0 ? 0 : 1);
+                const bool whole = info.flags & kWhole;
                 const float s = columns_sum<NC>(l, lane);
-                if (lane < NC) red_f[quad * NC + lane] = s;
+                if ((lane & 15) < NC) red_f[quad * NG + hq * NC + (lane & 15)] = s;
                 named_bar_sync(bar_id, 128);
-                const int h0 = w.g * NH + part * NC;
-                if (gt < NC) {
-                    const float sum = red_f[gt] + red_f[NC + gt] + red_f[2 * NC + gt] + red_f[3 * NC + gt];
+                const int h0 = info.g * NH + part * NG;
+                if (gt < NG) {
+                    const float sum = red_f[gt] + red_f[NG + gt] + red_f[2 * NG + gt] + red_f[3 * NG + gt];
                     fac[gt] = sum != 0.0f ? 1.0f / sum : 0.0f;
                     if (!whole) {
-                        float *ml = a.part_ml + ((int64_t)slot * NH + part * NC + gt) * 2;
-                        ml[0] = ref[gt];
+                        float *ml = a.part_ml + ((int64_t)info.slot * NH + part * NG + gt) * 2;
+                        ml[0] = -ref[gt];
                         ml[1] = sum;
                     } else if (a.lse && h0 + gt < a.Hq) {
-                        a.lse[(int64_t)w.b * a.Hq + h0 + gt] =
-                            sum != 0.0f ? (ref[gt] - P_OFFSET + log2f(sum)) * LN2 : -INFINITY;
+                        a.lse[(int64_t)info.b * a.Hq + h0 + gt] =
+                            sum != 0.0f ? (log2f(sum) - ref[gt]) * LN2 : -INFINITY;
                     }
                 }
                 named_bar_sync(bar_id, 128);
@@ -570,22 +671,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 tc_fence_after();
 #pragma unroll 1
                 for (int u = 0; u < U; u++) {
-                    float o[NC];
-                    tmem_load<NC>(tmem + lanes + u * NH + part * NC, o);
-                    const int c = 128 * u + key;
-                    if (c < a.C) {
+                    const int ch = 128 * u + quad * 32 + lane;
+#pragma unroll 1
+                    for (int c = 0; c < NG; c += W) {
+                        float o[W];
+                        tmem_load<W>(tmem + lanes + u * NH + part * NG + c, o);
+                        if (ch >= a.C) continue;
                         if (whole) {
-                            uint16_t *dst = a.out + ((int64_t)w.b * a.Hq + h0) * a.C + c;
+                            uint16_t *dst = a.out + ((int64_t)info.b * a.Hq + h0 + c) * a.C + ch;
 #pragma unroll
-                            for (int i = 0; i < NC; i++)
-                                if (h0 + i < a.Hq) {
-                                    const __nv_bfloat16 v = __float2bfloat16_rn(o[i] * fac[i]);
+                            for (int i = 0; i < W; i++)
+                                if (h0 + c + i < a.Hq) {
+                                    const __nv_bfloat16 v = __float2bfloat16_rn(o[i] * fac[c + i]);
                                     dst[(int64_t)i * a.C] = *reinterpret_cast<const uint16_t *>(&v);
                                 }
                         } else {
-                            float *dst = a.part_o + ((int64_t)slot * NH + part * NC) * (128 * U) + c;
+                            float *dst = a.part_o + ((int64_t)info.slot * NH + part * NG + c) * (128 * U) + ch;
 #pragma unroll
-                            for (int i = 0; i < NC; i++) dst[i * (128 * U)] = o[i];
+                            for (int i = 0; i < W; i++) dst[i * (128 * U)] = o[i];
                         }
                     }
                 }
@@ -594,51 +697,93 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(bar(L::B_OFREE));
                 seg++;
             }
-            w.next(a, k + 1 < n_tiles);
         }
     } else if (warp < MMA_WARP) {
         // ------------------------------------------------ loads and dequantization
+        // A warp has eight rows of the tile. Per unit a row is 64 bytes of codes: four
+        // lanes of 16 bytes, eight rows per access (a lane per row would touch 32
+        // lines an access). The lanes' order gives each eight of a store's lanes
+        // four rows and two pieces: all banks.
         const int lw = warp - NSOFT / 32;
-        const int half = lw & 1, rg = lw >> 1, r = rg * 32 + lane;  // chunk of the unit, key row
+        const int piece = (lane & 1) | (lane >> 4) << 1;      // 32 channels of a unit
+        const int r = lw * 8 + ((lane >> 1) & 7);             // key row
+        // in a unit: the row, and the swizzled place of its piece i: swap ^ (i << 4)
+        const uint32_t row_off = (piece >> 1) * CHUNK + (r >> 3) * 1024 + (r & 7) * 128;
+        const uint32_t swap = (uint32_t)(((piece & 1) * 4) ^ (r & 7)) << 4;
         bool ok = true;
         uint32_t seg = 0;
-        Ring<L::NU> ur;
-        uint4 code[U][2];   // the tile ahead: 64 channels of each unit
-        uint32_t scl[U];
+        Ring<L::NT> ur;
+        uint4 code[U];   // of the tile ahead
         const int row_bytes = a.C / 2, sf_bytes = a.C / (MX ? 32 : 16);
-        auto load_unit = [&](int u, int64_t row) {
-            const int c0 = 128 * u + 64 * half;
-            code[u][0] = code[u][1] = make_uint4(0, 0, 0, 0);
-            scl[u] = 0;
-            if (row >= 0 && c0 < a.C) {
-                const uint8_t *p = a.fp4 + row * row_bytes + c0 / 2;
-                const uint8_t *s = a.sf + row * sf_bytes;
-                const bool two = c0 + 32 < a.C;
-                code[u][0] = __ldg(reinterpret_cast<const uint4 *>(p));
-                if (two) code[u][1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-                if constexpr (MX) {
-                    scl[u] = __ldg(s + c0 / 32);
-                    if (two) scl[u] |= (uint32_t)__ldg(s + c0 / 32 + 1) << 8;
-                } else {
-                    const uint16_t *s2 = reinterpret_cast<const uint16_t *>(s + c0 / 16);
-                    scl[u] = __ldg(s2);
-                    if (two) scl[u] |= (uint32_t)__ldg(s2 + 1) << 16;
+        // Scales as loaded (anything done to them here would wait for the load). Wide:
+        // the four lanes of a row hold the scales of one unit each, eight or (MX) four
+        // bytes, and pass them round when that unit comes; one access per row and tile
+        // instead of one per row and unit. Otherwise: a lane's own, per unit.
+        const bool wide = a.wide_scales;
+        uint2 sw;
+        uint32_t scl[U];
+        auto load_tile = [&](int64_t row) {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int c0 = 128 * u + 32 * piece;
+                code[u] = make_uint4(0, 0, 0, 0);
+                if (row >= 0 && c0 < a.C)
+                    code[u] = __ldg(reinterpret_cast<const uint4 *>(a.fp4 + row * row_bytes + c0 / 2));
+            }
+            const uint8_t *s = a.sf + row * sf_bytes;
+            sw = make_uint2(0, 0);
+            if (wide) {
+                if (row >= 0 && 128 * piece < a.C) {
+                    if constexpr (MX)
+                        sw.x = __ldg(reinterpret_cast<const uint32_t *>(s + 4 * piece));
+                    else
+                        sw = __ldg(reinterpret_cast<const uint2 *>(s + 8 * piece));
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int c0 = 128 * u + 32 * piece;
+                    scl[u] = 0;
+                    if (row >= 0 && c0 < a.C)
+                        scl[u] = MX ? (uint32_t)__ldg(s + c0 / 32)
+                                    : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s + c0 / 16));
                 }
             }
         };
-        // tile k + 1's row is looked up one tile before its loads are issued
-        int64_t row = paged_row(a.pk, w.b, w.position(r));
-        bool here = row >= 0;
-#pragma unroll
-        for (int u = 0; u < U; u++) load_unit(u, row);
+        // the lane's scales of unit u: one E8M0 byte, or two E4M3
+        auto scales = [&](int u) {
+            if (!wide) return scl[u];
+            const int from = (lane & 14) | (u & 1) | (u >> 1) << 4;  // the row's lane with piece u
+            const uint32_t x = __shfl_sync(0xffffffffu, sw.x, from);
+            if constexpr (MX) return (x >> (8 * piece)) & 0xFF;
+            const uint32_t y = __shfl_sync(0xffffffffu, sw.y, from);
+            return ((piece & 2 ? y : x) >> (16 * (piece & 1))) & 0xFFFF;
+        };
+        // Table entries are read one tile before their rows are, and not looked at
+        // before: page and slot of the tile after the one in code[].
         Walk ahead = w;
-        int64_t row_next = -1;
+        int32_t page;
+        int slot;
+        auto look_up = [&]() {
+            const int pos = ahead.position(r);
+            const int e = pos < 0 ? 0 : (int)((uint32_t)pos / (uint32_t)a.pk.page_size);
+            slot = pos - e * a.pk.page_size;
+            page = pos < 0 ? -1 : __ldg(a.pk.table + (int64_t)ahead.b * a.pk.max_pages + e);
+        };
+        // of the tile whose loads go out, -1: no key
+        auto find_row = [&]() {
+            return page >= 0 && page < a.pk.n_pages ? (int64_t)page * a.pk.page_size + slot : (int64_t)-1;
+        };
+        look_up();
+        int64_t row = find_row();
+        load_tile(row);
+        bool here = row >= 0;
         if (n_tiles > 1) {
             ahead.next(a, true);
-            row_next = paged_row(a.pk, ahead.b, ahead.position(r));
+            look_up();
         }
         bool first = true;
-        for (int64_t k = 0; k < n_tiles; k++) {
+        for (int k = 0; k < n_tiles; k++) {
             if (first) {
                 // ---- queries of a new pair: one warp a head, lanes over channels
                 ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
@@ -688,130 +833,173 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(bar(L::B_QFULL));
                 seg++;
             }
-            first = w.tile + 1 == w.s.tiles;
-            const uint32_t seen = __ballot_sync(0xffffffffu, here);
-            const bool write = r < w.keys16();
-            // rows of the tile after the next, while the next one's loads go out
-            const int64_t row_load = row_next;
+            first = w.tile + 1 == w.s.tiles;  // the next tile starts a pair
+            const uint32_t seen = __ballot_sync(0xffffffffu, here);  // lanes 2 i (piece 0) hold rows i
+            const int keys = w.keys16();
+            if (k + 1 < n_tiles) row = find_row();
+            here = row >= 0;
             if (k + 2 < n_tiles) {
                 ahead.next(a, true);
-                row_next = paged_row(a.pk, ahead.b, ahead.position(r));
+                look_up();
             }
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                ok = wait_bar(bar(L::B_UFREE + ur.i), ur.phase ^ 1, abort) && ok;
-                if (u == 0 && half == 0 && lane == 0)
-                    reinterpret_cast<volatile uint32_t *>(sm + L::VALID_OFF)[(k % VALID_RING) * 4 + rg] = seen;
-                if (write && 128 * u + 64 * half < a.C) {
-                    const uint32_t dst = base + L::K_OFF + ur.i * UNIT + half * CHUNK;
-                    const uint32_t wd[8] = {code[u][0].x, code[u][0].y, code[u][0].z, code[u][0].w,
-                                            code[u][1].x, code[u][1].y, code[u][1].z, code[u][1].w};
-                    if constexpr (MX) {
-                        const MxScale s0 = mx_scale(scl[u] & 0xFF), s1 = mx_scale((scl[u] >> 8) & 0xFF);
+            for (int st = 0; st < L::NS; st++) {
+                ok = wait_bar(bar(L::B_UFREE + ur.i * L::NS + st), ur.phase ^ 1, abort) && ok;
+                if (st == 0 && lane == 0) {
+                    const uint32_t vi = (uint32_t)k % VALID_RING;
+                    uint32_t bits = 0;
 #pragma unroll
-                        for (int p = 0; p < 8; p++) st_shared_v4(dst + sw128(r, p), rows_bf16(wd[p], p < 4 ? s0 : s1));
-                    } else {
-                        uint32_t s01, s23;  // two f16 scales each
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s01) : "h"((uint16_t)scl[u]));
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s23) : "h"((uint16_t)(scl[u] >> 16)));
-                        const uint32_t s[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                                               __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-#pragma unroll
-                        for (int p = 0; p < 8; p++) st_shared_v4(dst + sw128(r, p), rows_f16(wd[p], s[p >> 1]));
+                    for (int i = 0; i < 8; i++) bits |= ((seen >> (2 * i)) & 1) << i;
+                    reinterpret_cast<volatile uint8_t *>(sm + L::VALID_OFF)[vi * 8 + lw] = (uint8_t)bits;
+                    if (lw == 0) {
+                        const bool from_start = w.tile <= k;  // the pair's first tile is this CTA's too
+                        const bool last = first || k + 1 == n_tiles;
+                        const int flags = (last ? kLast : 0) | (first && from_start ? kWhole : 0) | (keys / 16) << 8;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + L::INFO_OFF + 16 * vi),
+                                     "r"(w.b), "r"(w.g), "r"(flags), "r"(2 * cta + (w.tile < k ? 1 : 0))
+                                     : "memory");
                     }
                 }
-                if (k + 1 < n_tiles) load_unit(u, row_load);
+#pragma unroll
+                for (int u = 2 * st; u < 2 * st + 2 && u < U; u++) {
+                    const uint32_t sc = scales(u);
+                    if (8 * lw < keys && 128 * u + 32 * piece < a.C) {
+                        const uint32_t dst = base + L::K_OFF + (ur.i * U + u) * UNIT + row_off;
+                        const uint32_t wd[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+                        if constexpr (MX) {
+                            const MxScale s = mx_scale(sc);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) st_shared_v4(dst + (swap ^ (i << 4)), rows_bf16(wd[i], s));
+                        } else {
+                            uint32_t s01;  // the two groups' scales in f16
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s01) : "h"((uint16_t)sc));
+                            const uint32_t s[2] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232)};
+#pragma unroll
+                            for (int i = 0; i < 4; i++) st_shared_v4(dst + (swap ^ (i << 4)), rows_f16(wd[i], s[i >> 1]));
+                        }
+                    }
+                }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::B_UFULL + ur.i));
-                ur.next();
+                if (lane == 0) mbar_arrive(bar(L::B_UFULL + ur.i * L::NS + st));
             }
-            here = row_load >= 0;
+            ur.next();
+            // The next tile's loads, all at once when this one's registers are used up:
+            // loads still in flight hold up the fences above and any use of another
+            // load's registers. They have until this tile's P V to arrive.
+            if (k + 1 < n_tiles) load_tile(row);
             w.next(a, k + 1 < n_tiles);
         }
-    } else if (lane == 0) {
-        // ------------------------------------------------ MMA issue
-        constexpr uint32_t id_s = MX ? idesc_bf16(128, NH, false) : idesc_f16(128, NH, false);
+    } else {
+        // ------------------------------------------------ MMA issue: P V of the oldest
+        // tile when its weights are there, else the next step of S when its rows are.
+        // Neither wait may suspend the warp, it would wake for its own barrier alone.
+        // The warp stays together, so that descriptors are computed once for it, and
+        // one lane issues.
+        constexpr uint32_t id_s = MX ? idesc_bf16(TK, NH, false) : idesc_f16(TK, NH, false);
         constexpr uint32_t id_o = MX ? idesc_bf16(128, NH, true, true) : idesc_f16(128, NH, true, true);
         const uint64_t dq = sdesc(base + L::Q_OFF, 16, 1024);
         const uint64_t dk = sdesc(base + L::K_OFF, 16, 1024);
         const uint64_t dv = sdesc(base + L::K_OFF, CHUNK, 1024);
         const uint64_t dp = p_desc<NH>(base + L::P_OFF);
-        Walk ws = w, wp = w;  // of S and of P V
-        int64_t ks = 0, kp = 0;
-        int us = 0;                      // next unit of S
         bool s_first = true, p_first = true;
         uint32_t s_seg = 0, p_seg = 0;
-        Ring<2> sr;
-        Ring<L::NP> pr;
-        Ring<L::NU> su, pu;
-        uint64_t last_step = globaltimer_ns();
-        while (kp < n_tiles && !*abort) {
-            bool progressed = false;
-            const bool s_cand = ks < n_tiles && ks < kp + 2;
-            if (kp < ks) {
-                const bool ready = s_cand ? test_wait(bar(L::B_PFULL + pr.i), pr.phase)
-                                          : try_wait_hint(bar(L::B_PFULL + pr.i), pr.phase, 1000);
-                if (ready && (!p_first || test_wait(bar(L::B_OFREE), (p_seg & 1) ^ 1))) {
-                    tc_fence_after();
-                    const int steps = wp.keys16() / 16;
-                    const uint64_t p0 = dp + (uint64_t)((pr.i * L::PARTS * L::P_PART) >> 4);
+        Ring<2> sr, pr;
+        Ring<L::NT> su, pu;
+        int ks = 0, kp = 0, st = 0;  // next tile (and step) of S, next tile of P V
+        bool s_open = false;         // the next tile of S has its queries and its buffer
+        uint32_t idle = 0;
+        uint64_t idle_since = 0;
+        while (kp < n_tiles) {
+            if (kp < ks && __all_sync(0xffffffffu, test_wait(bar(L::B_PFULL + pr.i), pr.phase))) {
+                if (p_first && !__all_sync(0xffffffffu, wait_bar(bar(L::B_OFREE), (p_seg & 1) ^ 1, abort))) break;
+                tc_fence_after();
+                const int flags = read_info(base + L::INFO_OFF, (uint32_t)kp % VALID_RING).flags, steps = flags >> 8;
+                const bool last = flags & kLast;
+                const uint64_t p0 = dp + (uint64_t)((pr.i * L::PARTS * L::P_PART) >> 4);
+                const uint64_t v0 = dv + (uint64_t)((pu.i * U * UNIT) >> 4);
+                if (elect_one()) {
+#pragma unroll
                     for (int u = 0; u < U; u++) {
-                        const uint64_t v0 = dv + (uint64_t)((pu.i * UNIT) >> 4);
-                        for (int s = 0; s < steps; s++) {
-                            const uint64_t vd = v0 + (uint64_t)((s * 2048) >> 4);
+                        auto step = [&](int s, uint32_t acc) {
+                            const uint64_t vd = v0 + (uint64_t)((u * UNIT + s * 2048) >> 4);
                             const uint64_t pd = p0 + (uint64_t)((s * 16 * NH * 2) >> 4);
-                            mma_bf16(tmem + u * NH, vd, pd, id_o, !p_first || s > 0 ? 1u : 0u);
+                            mma_bf16(tmem + u * NH, vd, pd, id_o, acc);
                             if constexpr (MX) mma_bf16(tmem + u * NH, vd, pd + (uint64_t)(L::P_PART >> 4), id_o, 1u);
+                        };
+                        step(0, p_first ? 0u : 1u);
+                        if (steps == TK / 16) {
+#pragma unroll
+                            for (int s = 1; s < TK / 16; s++) step(s, 1u);
+                        } else {
+#pragma unroll 1
+                            for (int s = 1; s < steps; s++) step(s, 1u);
                         }
-                        mma_commit(bar(L::B_UFREE + pu.i));
-                        pu.next();
+                        if (u % 2 || u == U - 1) mma_commit(bar(L::B_UFREE + pu.i * L::NS + u / 2));
                     }
                     mma_commit(bar(L::B_PFREE + pr.i));
-                    pr.next();
-                    p_first = wp.tile + 1 == wp.s.tiles;
-                    if (p_first || kp + 1 == n_tiles) {
-                        mma_commit(bar(L::B_OFULL));
-                        p_seg++;
-                    }
-                    kp++;
-                    wp.next(a, kp < n_tiles);
-                    progressed = true;
+                    if (last) mma_commit(bar(L::B_OFULL));
                 }
+                __syncwarp();
+                pu.next();
+                pr.next();
+                p_first = last;
+                p_seg += last;
+                kp++;
+                idle = 0;
+                continue;
             }
-            if (!progressed && s_cand) {
-                if ((us > 0 || ((!s_first || test_wait(bar(L::B_QFULL), s_seg & 1)) &&
-                                test_wait(bar(L::B_SFREE + sr.i), sr.phase ^ 1))) &&
-                    try_wait_hint(bar(L::B_UFULL + su.i), su.phase, kp < ks ? 200 : 1000)) {
+            if (ks < n_tiles && ks < kp + 2) {
+                if (!s_open)
+                    s_open = __all_sync(0xffffffffu, (!s_first || test_wait(bar(L::B_QFULL), s_seg & 1)) &&
+                                                         test_wait(bar(L::B_SFREE + sr.i), sr.phase ^ 1));
+                if (s_open && __all_sync(0xffffffffu, test_wait(bar(L::B_UFULL + su.i * L::NS + st), su.phase))) {
                     tc_fence_after();
-                    const uint64_t k0 = dk + (uint64_t)((su.i * UNIT) >> 4);
-                    const uint64_t q0 = dq + (uint64_t)((us * 2 * L::Q_CHUNK) >> 4);
-                    const uint32_t sd = tmem + (U + sr.i) * NH;
-                    const int left = (a.C - 128 * us) / 16, steps = left < 8 ? left : 8;
-                    for (int s = 0; s < steps; s++)
-                        mma_bf16(sd, k0 + (uint64_t)(((s >> 2) * CHUNK + (s & 3) * 32) >> 4),
-                                 q0 + (uint64_t)(((s >> 2) * L::Q_CHUNK + (s & 3) * 32) >> 4), id_s,
-                                 us > 0 || s > 0 ? 1u : 0u);
-                    su.next();
-                    if (++us == U) {
-                        us = 0;
-                        mma_commit(bar(L::B_SFULL + sr.i));
-                        sr.next();
-                        s_first = ws.tile + 1 == ws.s.tiles;
-                        if (s_first) {
-                            mma_commit(bar(L::B_QFREE));
-                            s_seg++;
+                    const bool last = read_info(base + L::INFO_OFF, (uint32_t)ks % VALID_RING).flags & kLast;
+                    const uint64_t k0 = dk + (uint64_t)(((su.i * U + 2 * st) * UNIT) >> 4);
+                    const uint64_t q0 = dq + (uint64_t)((st * 4 * L::Q_CHUNK) >> 4);
+                    const uint32_t sd = tmem + ((16u * sr.i) << 16) + U * NH;
+                    const int left = (a.C - 256 * st) / 16;  // 16-channel MMAs, eight a unit
+                    if (elect_one()) {
+                        auto step = [&](int s, uint32_t acc) {
+                            mma_bf16(sd, k0 + (uint64_t)(((s >> 2) * CHUNK + (s & 3) * 32) >> 4),
+                                     q0 + (uint64_t)(((s >> 2) * L::Q_CHUNK + (s & 3) * 32) >> 4), id_s, acc);
+                        };
+                        step(0, st > 0 ? 1u : 0u);
+                        if (left >= 16) {
+#pragma unroll
+                            for (int s = 1; s < 16; s++) step(s, 1u);
+                        } else {
+#pragma unroll 1
+                            for (int s = 1; s < left; s++) step(s, 1u);
                         }
-                        ks++;
-                        ws.next(a, ks < n_tiles);
+                        if (st == L::NS - 1) {
+                            mma_commit(bar(L::B_SFULL + sr.i));
+                            if (last) mma_commit(bar(L::B_QFREE));
+                        }
                     }
-                    progressed = true;
+                    __syncwarp();
+                    if (++st == L::NS) {
+                        st = 0;
+                        s_open = false;
+                        su.next();
+                        sr.next();
+                        s_first = last;
+                        s_seg += last;
+                        ks++;
+                    }
+                    idle = 0;
+                    continue;
                 }
             }
-            if (progressed) {
-                last_step = globaltimer_ns();
-            } else if (globaltimer_ns() - last_step > WAIT_NS) {
-                raise_abort(abort);
+            if ((++idle & 1023) == 0) {  // the timer is slow to read
+                if (__any_sync(0xffffffffu, *abort != 0)) break;
+                const uint64_t now = globaltimer_ns();
+                if (idle == 1024) {
+                    idle_since = now;
+                } else if (__any_sync(0xffffffffu, now - idle_since > WAIT_NS)) {
+                    raise_abort(abort);
+                }
             }
         }
     }

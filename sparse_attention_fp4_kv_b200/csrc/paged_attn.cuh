@@ -44,9 +44,26 @@
 
 #include "paged.cuh"
 #include "tcgen05.cuh"
+#include "tma.cuh"
+
+#include <type_traits>
 
 namespace csa2 {
 namespace pa {
+
+// n / d for 0 <= n < 2^31 by a product (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication"): m = 2^(31 + s) / d rounded up with
+// 2^s >= d is exact for such n, and below 2^32.
+struct FastDiv {
+    uint32_t m, s;
+    __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
+};
+inline FastDiv fast_div(int d) {
+    FastDiv f{0, 0};
+    while ((1ll << f.s) < d) f.s++;
+    f.m = (uint32_t)(((1ull << (31 + f.s)) + (uint64_t)d - 1) / (uint64_t)d);
+    return f;
+}
 
 struct Args {
     const uint16_t *q;
@@ -55,6 +72,7 @@ struct Args {
     const int64_t *ctx_len;
     int win, sink;         // 0: every position
     int cap;               // max_pages * page_size
+    FastDiv page_div;      // by page_size
     int B, Hq, C, groups;  // groups of NH heads
     bool wide_scales;      // a unit's scales of a row start on their size
     float scale;
@@ -70,8 +88,8 @@ struct Args {
 constexpr int TK = 64;              // keys per tile
 constexpr int CHUNK = TK * 128;     // 64 channels of a tile: rows of 128 bytes
 constexpr int UNIT = 2 * CHUNK;
-constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 32;
-constexpr int MMA_WARP = (NSOFT + NLOAD) / 32;
+constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 64;
+constexpr int S_WARP = (NSOFT + NLOAD) / 32;
 constexpr int MAX_RING = 8;          // tiles of the ring, and steps
 constexpr int VALID_RING = 16, QF_RING = 3;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -108,12 +126,17 @@ __device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (i
 template <bool MX, int U, int NH>
 struct Layout {
     static constexpr int PARTS = MX ? 2 : 1;       // of the weights
-    static constexpr int NP = 2;                   // buffers of weights
+    static constexpr bool FULL = U == 4 && NH == 64;          // the shape that fills shared memory
+    static constexpr int NP = FULL ? 1 : 2;                   // buffers of weights
     static constexpr int P_PART = TK * NH * 2;
     static constexpr int Q_CHUNK = NH * 128;       // 64 channels of Q
     static constexpr int Q_OFF = 0;
     static constexpr int P_OFF = Q_OFF + 2 * U * Q_CHUNK;
-    static constexpr int K_OFF = P_OFF + NP * PARTS * P_PART;
+    // codes as they come from the pages, a row's 64 U bytes apart by 32 more where they
+    // fit: eight lanes that read two pieces of four rows then fall on all banks
+    static constexpr int RAW_PITCH = 64 * U + (FULL && MX ? 0 : 32);
+    static constexpr int RAW_OFF = P_OFF + NP * PARTS * P_PART;
+    static constexpr int K_OFF = (RAW_OFF + TK * RAW_PITCH + 1023) / 1024 * 1024;
     static constexpr int SMALL = 3072;
     static constexpr int FIT = (227 * 1024 - SMALL - K_OFF) / (U * UNIT);
     static constexpr int NS = (U + 1) / 2;                 // steps of a tile: two units each, the last maybe one
@@ -128,7 +151,8 @@ struct Layout {
     static constexpr int BAR_OFF = INFO_OFF + VALID_RING * 16;
     static constexpr int B_QFULL = 0, B_QFREE = 1, B_UFULL = 2, B_UFREE = B_UFULL + MAX_RING,
                          B_SFULL = B_UFREE + MAX_RING, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
-                         B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1, NBARS = B_OFREE + 1;
+                         B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1, B_RAW = B_OFREE + 1,
+                         NBARS = B_RAW + NLOAD / 32;
     static constexpr int START_OFF = BAR_OFF + NBARS * 8; // int64 first offset, count; int pair
     static constexpr int TADDR_OFF = START_OFF + 24;
     static constexpr int ABORT_OFF = TADDR_OFF + 4;
@@ -289,6 +313,21 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(0x80008000u));
     return r;
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+// `bytes` (a multiple of 16, from a 16-byte boundary to one) into shared memory,
+// counted by the barrier.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 // Eight codes -> four pairs of f16 values of E2M1.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
     asm("{\n.reg .b8 b0, b1, b2, b3;\nmov.b32 {b0, b1, b2, b3}, %4;\n"
@@ -435,10 +474,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         }
         mbar_init(bar(L::B_OFULL), 1);
         mbar_init(bar(L::B_OFREE), NSOFT / 32);
+        for (int i = 0; i < NLOAD / 32; i++) mbar_init(bar(L::B_RAW + i), 1);
         *abort = (base & 1023u) != 0;  // the swizzles want this alignment
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == MMA_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
+    if (warp == S_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
 
     // ---- this CTA's share of the tiles: totals, then where its first tile lies
     int64_t *red = reinterpret_cast<int64_t *>(sm + L::RED_OFF);  // [17], and the total at [31]
@@ -515,7 +555,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         bool ok = true, first = true;
         float l[NC];
         uint32_t seg = 0;
-        Ring<2> sr, pr;
+        Ring<2> sr;
+        Ring<L::NP> pr;
         Ring<L::NT> ur;
         for (int k = 0; k < n_tiles; k++) {
             if (first) {
@@ -530,38 +571,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             const TileInfo info = read_info(base + L::INFO_OFF, vi);
             const uint32_t seen = ok ? valid[vi * 4 + quad] : 0u;
             const bool see = (seen >> (lane & 15)) & 1;
-            float f[NC];
-#pragma unroll
-            for (int i = 0; i < NC; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(qf + i);
-                f[i] = v.x;
-                f[i + 1] = v.y;
-                f[i + 2] = v.z;
-                f[i + 3] = v.w;
-            }
             ok = wait_bar(bar(L::B_SFULL + sr.i), sr.phase, abort) && ok;
             tc_fence_after();
+            // x becomes the exponents x f + (7 - reference)
             float x[NC];
-            tmem_load_half<NC>(tmem + lanes + ((16u * sr.i) << 16) + U * NH + part * NG, x);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::B_SFREE + sr.i));
+            auto exponents = [&]() {
+                tmem_load_half<NC>(tmem + lanes + ((16u * sr.i) << 16) + U * NH + part * NG, x);
+#pragma unroll
+                for (int i = 0; i < NC; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qf + i);
+                    const float4 r = *reinterpret_cast<const float4 *>(rq + i);
+                    x[i] = fmaf(x[i], f.x, r.x);
+                    x[i + 1] = fmaf(x[i + 1], f.y, r.y);
+                    x[i + 2] = fmaf(x[i + 2], f.z, r.z);
+                    x[i + 3] = fmaf(x[i + 3], f.w, r.w);
+                }
+            };
             // ---- does a score exceed its head's reference by 2^8?
             bool move = first;
             if (!first) {
-                float over = -INFINITY;
+                exponents();
+                float over = x[0];
 #pragma unroll
-                for (int i = 0; i < NC; i += 4) {
-                    const float4 r = *reinterpret_cast<const float4 *>(rq + i);
-                    over = fmaxf(over, fmaxf(fmaf(x[i], f[i], r.x), fmaf(x[i + 1], f[i + 1], r.y)));
-                    over = fmaxf(over, fmaxf(fmaf(x[i + 2], f[i + 2], r.z), fmaf(x[i + 3], f[i + 3], r.w)));
-                }
+                for (int i = 1; i < NC; i++) over = fmaxf(over, x[i]);
                 move = named_bar_or(bar_id, 128, see && over > RESCALE_LOG2 + P_OFFSET);
             }
             if (move) {
+                // rare: the scores are read again
                 float y[NC];
+                tmem_load_half<NC>(tmem + lanes + ((16u * sr.i) << 16) + U * NH + part * NG, y);
 #pragma unroll
-                for (int i = 0; i < NC; i++) y[i] = see ? x[i] * f[i] : -INFINITY;
+                for (int i = 0; i < NC; i++) y[i] = see ? y[i] * qf[i] : -INFINITY;
                 const float mine = columns_max<NC>(y, lane);
                 if ((lane & 15) < NC) red_f[quad * NG + hq * NC + (lane & 15)] = mine;
                 named_bar_sync(bar_id, 128);
@@ -575,10 +615,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 }
                 named_bar_sync(bar_id, 128);
             }
-            // this buffer's last P V is done; a rescale waits for the other one's too
+            // this buffer's last P V is done, and with one buffer so is the last
+            // tile's; with two, a rescale waits for the other one too
             ok = wait_bar(bar(L::B_PFREE + pr.i), pr.phase ^ 1, abort) && ok;
+            if (move) exponents();  // with the new references
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::B_SFREE + sr.i));
             if (move && !first) {
-                ok = wait_bar(bar(L::B_PFREE + (pr.i ^ 1)), pr.i ? pr.phase : pr.phase ^ 1, abort) && ok;
+                if constexpr (L::NP == 2)
+                    ok = wait_bar(bar(L::B_PFREE + (pr.i ^ 1)), pr.i ? pr.phase : pr.phase ^ 1, abort) && ok;
                 tc_fence_after();
 #pragma unroll 1
                 for (int u = 0; u < U; u++)
@@ -597,13 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             }
             const uint32_t pb = base + L::P_OFF + pr.i * L::PARTS * L::P_PART;
 #pragma unroll
-            for (int i = 0; i < NC; i += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(rq + i);
-                x[i] = ex2(fmaf(x[i], f[i], r.x));
-                x[i + 1] = ex2(fmaf(x[i + 1], f[i + 1], r.y));
-                x[i + 2] = ex2(fmaf(x[i + 2], f[i + 2], r.z));
-                x[i + 3] = ex2(fmaf(x[i + 3], f[i + 3], r.w));
-            }
+            for (int i = 0; i < NC; i++) x[i] = ex2(x[i]);
             if (!see) {  // a row without a key may hold anything
 #pragma unroll
                 for (int i = 0; i < NC; i++) x[i] = 0.0f;
@@ -698,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 seg++;
             }
         }
-    } else if (warp < MMA_WARP) {
+    } else if (warp < S_WARP) {
         // ------------------------------------------------ loads and dequantization
         // A warp has eight rows of the tile. Per unit a row is 64 bytes of codes: four
         // lanes of 16 bytes, eight rows per access (a lane per row would touch 32
@@ -713,8 +753,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         bool ok = true;
         uint32_t seg = 0;
         Ring<L::NT> ur;
-        uint4 code[U];   // of the tile ahead
+        // Codes come by bulk copies of whole rows into this warp's eight of the raw
+        // buffer, issued by the lanes of piece 0 as soon as the last tile's codes are in
+        // registers: through the load pipe they cost as much as all else a tile does
+        // there (265 against 200 us for 8 x 128K).
         const int row_bytes = a.C / 2, sf_bytes = a.C / (MX ? 32 : 16);
+        const uint32_t raw = base + L::RAW_OFF + r * L::RAW_PITCH, raw_bar = bar(L::B_RAW + lw);
+        auto copy_rows = [&](int64_t row) {
+            const uint32_t rows = __ballot_sync(0xffffffffu, row >= 0 && piece == 0);
+            if (lane == 0) mbar_expect_tx(raw_bar, __popc(rows) * row_bytes);
+            __syncwarp();
+            if (row >= 0 && piece == 0) bulk_copy(raw, a.fp4 + row * row_bytes, row_bytes, raw_bar);
+        };
         // Scales as loaded (anything done to them here would wait for the load). Wide:
         // the four lanes of a row hold the scales of one unit each, eight or (MX) four
         // bytes, and pass them round when that unit comes; one access per row and tile
@@ -722,14 +772,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         const bool wide = a.wide_scales;
         uint2 sw;
         uint32_t scl[U];
-        auto load_tile = [&](int64_t row) {
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int c0 = 128 * u + 32 * piece;
-                code[u] = make_uint4(0, 0, 0, 0);
-                if (row >= 0 && c0 < a.C)
-                    code[u] = __ldg(reinterpret_cast<const uint4 *>(a.fp4 + row * row_bytes + c0 / 2));
-            }
+        auto load_scales = [&](int64_t row) {
             const uint8_t *s = a.sf + row * sf_bytes;
             sw = make_uint2(0, 0);
             if (wide) {
@@ -759,31 +802,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             const uint32_t y = __shfl_sync(0xffffffffu, sw.y, from);
             return ((piece & 2 ? y : x) >> (16 * (piece & 1))) & 0xFFFF;
         };
-        // Table entries are read one tile before their rows are, and not looked at
-        // before: page and slot of the tile after the one in code[].
+        // A tile's table entries are read a tile before its rows. Whatever has to wait
+        // for a result stands before the loads go out: with six scoreboards a division
+        // behind them waits for them.
         Walk ahead = w;
         int32_t page;
         int slot;
         auto look_up = [&]() {
             const int pos = ahead.position(r);
-            const int e = pos < 0 ? 0 : (int)((uint32_t)pos / (uint32_t)a.pk.page_size);
+            const int e = pos < 0 ? 0 : a.page_div(pos);
             slot = pos - e * a.pk.page_size;
             page = pos < 0 ? -1 : __ldg(a.pk.table + (int64_t)ahead.b * a.pk.max_pages + e);
         };
-        // of the tile whose loads go out, -1: no key
-        auto find_row = [&]() {
+        auto find_row = [&]() {  // -1: no key
             return page >= 0 && page < a.pk.n_pages ? (int64_t)page * a.pk.page_size + slot : (int64_t)-1;
         };
         look_up();
-        int64_t row = find_row();
-        load_tile(row);
-        bool here = row >= 0;
+        int64_t row = find_row(), row_next = -1;  // of this tile and of the next
+        copy_rows(row);
         if (n_tiles > 1) {
             ahead.next(a, true);
             look_up();
+            row_next = find_row();
         }
+        if (n_tiles > 2) {
+            ahead.next(a, true);
+            look_up();
+        }
+        load_scales(row);
         bool first = true;
         for (int k = 0; k < n_tiles; k++) {
+            const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0);  // lanes 2 i (piece 0) hold rows i
             if (first) {
                 // ---- queries of a new pair: one warp a head, lanes over channels
                 ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
@@ -834,22 +883,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 seg++;
             }
             first = w.tile + 1 == w.s.tiles;  // the next tile starts a pair
-            const uint32_t seen = __ballot_sync(0xffffffffu, here);  // lanes 2 i (piece 0) hold rows i
             const int keys = w.keys16();
-            if (k + 1 < n_tiles) row = find_row();
-            here = row >= 0;
-            if (k + 2 < n_tiles) {
-                ahead.next(a, true);
-                look_up();
+            ok = wait_bar(raw_bar, k & 1, abort) && ok;
+            uint4 code[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                code[u] = make_uint4(0, 0, 0, 0);
+                if (row >= 0) code[u] = ld_shared_v4(raw + 64 * u + 16 * piece);
             }
+            fence_proxy_async();  // these reads before the next copies' writes
+            __syncwarp();
+            if (k + 1 < n_tiles) copy_rows(row_next);
 #pragma unroll
             for (int st = 0; st < L::NS; st++) {
                 ok = wait_bar(bar(L::B_UFREE + ur.i * L::NS + st), ur.phase ^ 1, abort) && ok;
                 if (st == 0 && lane == 0) {
                     const uint32_t vi = (uint32_t)k % VALID_RING;
-                    uint32_t bits = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) bits |= ((seen >> (2 * i)) & 1) << i;
+                    uint32_t bits = seen & 0x5555u;  // every other bit, drawn together
+                    bits = (bits | bits >> 1) & 0x3333u;
+                    bits = (bits | bits >> 2) & 0x0F0Fu;
+                    bits |= bits >> 4;
                     reinterpret_cast<volatile uint8_t *>(sm + L::VALID_OFF)[vi * 8 + lw] = (uint8_t)bits;
                     if (lw == 0) {
                         const bool from_start = w.tile <= k;  // the pair's first tile is this CTA's too
@@ -884,123 +937,114 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(bar(L::B_UFULL + ur.i * L::NS + st));
             }
             ur.next();
-            // The next tile's loads, all at once when this one's registers are used up:
-            // loads still in flight hold up the fences above and any use of another
-            // load's registers. They have until this tile's P V to arrive.
-            if (k + 1 < n_tiles) load_tile(row);
+            row = row_next;
+            row_next = k + 2 < n_tiles ? find_row() : -1;
+            if (k + 3 < n_tiles) {
+                ahead.next(a, true);
+                look_up();
+            }
+            // after this tile's last fence, which would wait for them
+            if (k + 1 < n_tiles) load_scales(row);
             w.next(a, k + 1 < n_tiles);
         }
-    } else {
-        // ------------------------------------------------ MMA issue: P V of the oldest
-        // tile when its weights are there, else the next step of S when its rows are.
-        // Neither wait may suspend the warp, it would wake for its own barrier alone.
-        // The warp stays together, so that descriptors are computed once for it, and
-        // one lane issues.
-        constexpr uint32_t id_s = MX ? idesc_bf16(TK, NH, false) : idesc_f16(TK, NH, false);
-        constexpr uint32_t id_o = MX ? idesc_bf16(128, NH, true, true) : idesc_f16(128, NH, true, true);
+    } else if (warp == S_WARP) {
+        // ------------------------------------------------ issue of S. The two issuing
+        // warps each wait for their own barriers, suspended: one warp that watched both
+        // kept the shared-memory pipe busy with its polls. A warp stays together, so that
+        // descriptors are computed once for it, and one lane issues.
+        constexpr uint32_t id = MX ? idesc_bf16(TK, NH, false) : idesc_f16(TK, NH, false);
         const uint64_t dq = sdesc(base + L::Q_OFF, 16, 1024);
         const uint64_t dk = sdesc(base + L::K_OFF, 16, 1024);
-        const uint64_t dv = sdesc(base + L::K_OFF, CHUNK, 1024);
-        const uint64_t dp = p_desc<NH>(base + L::P_OFF);
-        bool s_first = true, p_first = true;
-        uint32_t s_seg = 0, p_seg = 0;
-        Ring<2> sr, pr;
-        Ring<L::NT> su, pu;
-        int ks = 0, kp = 0, st = 0;  // next tile (and step) of S, next tile of P V
-        bool s_open = false;         // the next tile of S has its queries and its buffer
-        uint32_t idle = 0;
-        uint64_t idle_since = 0;
-        while (kp < n_tiles) {
-            if (kp < ks && __all_sync(0xffffffffu, test_wait(bar(L::B_PFULL + pr.i), pr.phase))) {
-                if (p_first && !__all_sync(0xffffffffu, wait_bar(bar(L::B_OFREE), (p_seg & 1) ^ 1, abort))) break;
-                tc_fence_after();
-                const int flags = read_info(base + L::INFO_OFF, (uint32_t)kp % VALID_RING).flags, steps = flags >> 8;
-                const bool last = flags & kLast;
-                const uint64_t p0 = dp + (uint64_t)((pr.i * L::PARTS * L::P_PART) >> 4);
-                const uint64_t v0 = dv + (uint64_t)((pu.i * U * UNIT) >> 4);
-                if (elect_one()) {
-#pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        auto step = [&](int s, uint32_t acc) {
-                            const uint64_t vd = v0 + (uint64_t)((u * UNIT + s * 2048) >> 4);
-                            const uint64_t pd = p0 + (uint64_t)((s * 16 * NH * 2) >> 4);
-                            mma_bf16(tmem + u * NH, vd, pd, id_o, acc);
-                            if constexpr (MX) mma_bf16(tmem + u * NH, vd, pd + (uint64_t)(L::P_PART >> 4), id_o, 1u);
-                        };
-                        step(0, p_first ? 0u : 1u);
-                        if (steps == TK / 16) {
-#pragma unroll
-                            for (int s = 1; s < TK / 16; s++) step(s, 1u);
-                        } else {
+        bool ok = true, first = true;
+        uint32_t seg = 0;
+        Ring<2> sr;
+        Ring<L::NT> ur;
+        for (int k = 0; k < n_tiles && ok; k++) {
+            if (first) ok = wait_bar(bar(L::B_QFULL), seg & 1, abort) && ok;
+            ok = wait_bar(bar(L::B_SFREE + sr.i), sr.phase ^ 1, abort) && ok;
+            const uint32_t sd = tmem + ((16u * sr.i) << 16) + U * NH;
+            bool last = false;
 #pragma unroll 1
-                            for (int s = 1; s < steps; s++) step(s, 1u);
-                        }
-                        if (u % 2 || u == U - 1) mma_commit(bar(L::B_UFREE + pu.i * L::NS + u / 2));
+            for (int st = 0; st < L::NS; st++) {
+                ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS + st), ur.phase, abort) && ok;
+                if (st == 0) last = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING).flags & kLast;
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t k0 = dk + (uint64_t)(((ur.i * U + 2 * st) * UNIT) >> 4);
+                const uint64_t q0 = dq + (uint64_t)((st * 4 * L::Q_CHUNK) >> 4);
+                const int left = (a.C - 256 * st) / 16;  // 16-channel MMAs, eight a unit
+                if (elect_one()) {
+                    auto step = [&](int s, uint32_t acc) {
+                        mma_bf16(sd, k0 + (uint64_t)(((s >> 2) * CHUNK + (s & 3) * 32) >> 4),
+                                 q0 + (uint64_t)(((s >> 2) * L::Q_CHUNK + (s & 3) * 32) >> 4), id, acc);
+                    };
+                    step(0, st > 0 ? 1u : 0u);
+                    if (left >= 16) {
+#pragma unroll
+                        for (int s = 1; s < 16; s++) step(s, 1u);
+                    } else {
+#pragma unroll 1
+                        for (int s = 1; s < left; s++) step(s, 1u);
                     }
-                    mma_commit(bar(L::B_PFREE + pr.i));
-                    if (last) mma_commit(bar(L::B_OFULL));
+                    if (st == L::NS - 1) {
+                        mma_commit(bar(L::B_SFULL + sr.i));
+                        if (last) mma_commit(bar(L::B_QFREE));
+                    }
                 }
                 __syncwarp();
-                pu.next();
-                pr.next();
-                p_first = last;
-                p_seg += last;
-                kp++;
-                idle = 0;
-                continue;
             }
-            if (ks < n_tiles && ks < kp + 2) {
-                if (!s_open)
-                    s_open = __all_sync(0xffffffffu, (!s_first || test_wait(bar(L::B_QFULL), s_seg & 1)) &&
-                                                         test_wait(bar(L::B_SFREE + sr.i), sr.phase ^ 1));
-                if (s_open && __all_sync(0xffffffffu, test_wait(bar(L::B_UFULL + su.i * L::NS + st), su.phase))) {
-                    tc_fence_after();
-                    const bool last = read_info(base + L::INFO_OFF, (uint32_t)ks % VALID_RING).flags & kLast;
-                    const uint64_t k0 = dk + (uint64_t)(((su.i * U + 2 * st) * UNIT) >> 4);
-                    const uint64_t q0 = dq + (uint64_t)((st * 4 * L::Q_CHUNK) >> 4);
-                    const uint32_t sd = tmem + ((16u * sr.i) << 16) + U * NH;
-                    const int left = (a.C - 256 * st) / 16;  // 16-channel MMAs, eight a unit
-                    if (elect_one()) {
-                        auto step = [&](int s, uint32_t acc) {
-                            mma_bf16(sd, k0 + (uint64_t)(((s >> 2) * CHUNK + (s & 3) * 32) >> 4),
-                                     q0 + (uint64_t)(((s >> 2) * L::Q_CHUNK + (s & 3) * 32) >> 4), id_s, acc);
-                        };
-                        step(0, st > 0 ? 1u : 0u);
-                        if (left >= 16) {
+            ur.next();
+            sr.next();
+            first = last;
+            seg += last;
+        }
+    } else {
+        // ------------------------------------------------ issue of P V
+        constexpr uint32_t id = MX ? idesc_bf16(128, NH, true, true) : idesc_f16(128, NH, true, true);
+        const uint64_t dv = sdesc(base + L::K_OFF, CHUNK, 1024);
+        const uint64_t dp = p_desc<NH>(base + L::P_OFF);
+        bool ok = true, first = true;
+        uint32_t seg = 0;
+        Ring<L::NP> pr;
+        Ring<L::NT> ur;
+        for (int k = 0; k < n_tiles && ok; k++) {
+            // the softmax warps' barrier carries the load warps' info on to here
+            ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS), ur.phase, abort) && ok;
+            const int flags = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING).flags, steps = flags >> 8;
+            const bool last = flags & kLast;
+            if (first) ok = wait_bar(bar(L::B_OFREE), (seg & 1) ^ 1, abort) && ok;
+            ok = wait_bar(bar(L::B_PFULL + pr.i), pr.phase, abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t p0 = dp + (uint64_t)((pr.i * L::PARTS * L::P_PART) >> 4);
+            const uint64_t v0 = dv + (uint64_t)((ur.i * U * UNIT) >> 4);
+            if (elect_one()) {
 #pragma unroll
-                            for (int s = 1; s < 16; s++) step(s, 1u);
-                        } else {
+                for (int u = 0; u < U; u++) {
+                    auto step = [&](int s, uint32_t acc) {
+                        const uint64_t vd = v0 + (uint64_t)((u * UNIT + s * 2048) >> 4);
+                        const uint64_t pd = p0 + (uint64_t)((s * 16 * NH * 2) >> 4);
+                        mma_bf16(tmem + u * NH, vd, pd, id, acc);
+                        if constexpr (MX) mma_bf16(tmem + u * NH, vd, pd + (uint64_t)(L::P_PART >> 4), id, 1u);
+                    };
+                    step(0, first ? 0u : 1u);
+                    if (steps == TK / 16) {
+#pragma unroll
+                        for (int s = 1; s < TK / 16; s++) step(s, 1u);
+                    } else {
 #pragma unroll 1
-                            for (int s = 1; s < left; s++) step(s, 1u);
-                        }
-                        if (st == L::NS - 1) {
-                            mma_commit(bar(L::B_SFULL + sr.i));
-                            if (last) mma_commit(bar(L::B_QFREE));
-                        }
+                        for (int s = 1; s < steps; s++) step(s, 1u);
                     }
-                    __syncwarp();
-                    if (++st == L::NS) {
-                        st = 0;
-                        s_open = false;
-                        su.next();
-                        sr.next();
-                        s_first = last;
-                        s_seg += last;
-                        ks++;
-                    }
-                    idle = 0;
-                    continue;
+                    if (u % 2 || u == U - 1) mma_commit(bar(L::B_UFREE + ur.i * L::NS + u / 2));
                 }
+                mma_commit(bar(L::B_PFREE + pr.i));
+                if (last) mma_commit(bar(L::B_OFULL));
             }
-            if ((++idle & 1023) == 0) {  // the timer is slow to read
-                if (__any_sync(0xffffffffu, *abort != 0)) break;
-                const uint64_t now = globaltimer_ns();
-                if (idle == 1024) {
-                    idle_since = now;
-                } else if (__any_sync(0xffffffffu, now - idle_since > WAIT_NS)) {
-                    raise_abort(abort);
-                }
-            }
+            __syncwarp();
+            ur.next();
+            pr.next();
+            first = last;
+            seg += last;
         }
     }
     __syncthreads();
@@ -1011,7 +1055,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         while (globaltimer_ns() - t0 < 2000000ull) {
         }
     }
-    if (warp == MMA_WARP) {
+    if (warp == S_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, L::COLS);
     }

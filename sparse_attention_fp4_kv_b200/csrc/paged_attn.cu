@@ -157,8 +157,7 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
     if (!aligned(ws, 16)) return CSA2_ERR_ALIGN;
     cudaStream_t s = (cudaStream_t)stream;
     const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len,
-                 (int)(n_win < cap ? n_win : cap), (int)(n_sink < cap ? n_sink : cap), (int)cap, fast_div(page_size), B, Hq, C, groups,
-                 C % 128 == 0 && aligned(sf, mx ? 4 : 8), scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
+                 (int)(n_win < cap ? n_win : cap), (int)(n_sink < cap ? n_sink : cap), (int)cap, fast_div(page_size), B, Hq, C, groups, scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
     const int st = mx ? launch_paged_attn_mxfp4(a, nh, G, s) : launch_paged_attn_fp4(a, nh, G, s);
     if (st != CSA2_OK) return st;
     // one head per block until there are a few blocks per SM

@@ -44,7 +44,6 @@
 
 #include "paged.cuh"
 #include "tcgen05.cuh"
-#include "tma.cuh"
 
 #include <type_traits>
 
@@ -74,7 +73,6 @@ struct Args {
     int cap;               // max_pages * page_size
     FastDiv page_div;      // by page_size
     int B, Hq, C, groups;  // groups of NH heads
-    bool wide_scales;      // a unit's scales of a row start on their size
     float scale;
     uint16_t *out;
     float *lse;
@@ -88,8 +86,10 @@ struct Args {
 constexpr int TK = 64;              // keys per tile
 constexpr int CHUNK = TK * 128;     // 64 channels of a tile: rows of 128 bytes
 constexpr int UNIT = 2 * CHUNK;
-constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 64;
-constexpr int S_WARP = (NSOFT + NLOAD) / 32;
+constexpr int NSOFT = 256, NLOAD = 256, THREADS = NSOFT + NLOAD + 96;
+constexpr int LOAD_WARPS = NLOAD / 32;
+constexpr int S_WARP = (NSOFT + NLOAD) / 32, PV_WARP = S_WARP + 1, SCOUT_WARP = S_WARP + 2;
+constexpr int ROW_RING = 4;          // tiles whose rows the scout has found ahead
 constexpr int MAX_RING = 8;          // tiles of the ring, and steps
 constexpr int VALID_RING = 16, QF_RING = 3;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -126,18 +126,13 @@ __device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (i
 template <bool MX, int U, int NH>
 struct Layout {
     static constexpr int PARTS = MX ? 2 : 1;       // of the weights
-    static constexpr bool FULL = U == 4 && NH == 64;          // the shape that fills shared memory
-    static constexpr int NP = FULL ? 1 : 2;                   // buffers of weights
+    static constexpr int NP = MX && U == 4 && NH == 64 ? 1 : 2;  // buffers of weights
     static constexpr int P_PART = TK * NH * 2;
     static constexpr int Q_CHUNK = NH * 128;       // 64 channels of Q
     static constexpr int Q_OFF = 0;
     static constexpr int P_OFF = Q_OFF + 2 * U * Q_CHUNK;
-    // codes as they come from the pages, a row's 64 U bytes apart by 32 more where they
-    // fit: eight lanes that read two pieces of four rows then fall on all banks
-    static constexpr int RAW_PITCH = 64 * U + (FULL && MX ? 0 : 32);
-    static constexpr int RAW_OFF = P_OFF + NP * PARTS * P_PART;
-    static constexpr int K_OFF = (RAW_OFF + TK * RAW_PITCH + 1023) / 1024 * 1024;
-    static constexpr int SMALL = 3072;
+    static constexpr int K_OFF = P_OFF + NP * PARTS * P_PART;
+    static constexpr int SMALL = 5120;
     static constexpr int FIT = (227 * 1024 - SMALL - K_OFF) / (U * UNIT);
     static constexpr int NS = (U + 1) / 2;                 // steps of a tile: two units each, the last maybe one
     static constexpr int NT = FIT * NS < MAX_RING ? FIT : MAX_RING / NS;  // tiles of the ring
@@ -148,11 +143,12 @@ struct Layout {
     static constexpr int RED_OFF = FAC_OFF + NH * 4;      // fp32 [8][32]
     static constexpr int VALID_OFF = RED_OFF + 1024;      // a bit per key, 64 bits [VALID_RING]
     static constexpr int INFO_OFF = VALID_OFF + VALID_RING * 8;  // int4 [VALID_RING]
-    static constexpr int BAR_OFF = INFO_OFF + VALID_RING * 16;
+    static constexpr int ROW_OFF = INFO_OFF + VALID_RING * 16;    // int64 [ROW_RING][TK]: rows of the pool, -1: no key
+    static constexpr int BAR_OFF = ROW_OFF + ROW_RING * TK * 8;
     static constexpr int B_QFULL = 0, B_QFREE = 1, B_UFULL = 2, B_UFREE = B_UFULL + MAX_RING,
                          B_SFULL = B_UFREE + MAX_RING, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
-                         B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1, B_RAW = B_OFREE + 1,
-                         NBARS = B_RAW + NLOAD / 32;
+                         B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1,
+                         B_RFULL = B_OFREE + 1, B_RFREE = B_RFULL + ROW_RING, NBARS = B_RFREE + ROW_RING;
     static constexpr int START_OFF = BAR_OFF + NBARS * 8; // int64 first offset, count; int pair
     static constexpr int TADDR_OFF = START_OFF + 24;
     static constexpr int ABORT_OFF = TADDR_OFF + 4;
@@ -313,21 +309,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(0x80008000u));
     return r;
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-// `bytes` (a multiple of 16, from a 16-byte boundary to one) into shared memory,
-// counted by the barrier.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 // Eight codes -> four pairs of f16 values of E2M1.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
     asm("{\n.reg .b8 b0, b1, b2, b3;\nmov.b32 {b0, b1, b2, b3}, %4;\n"
@@ -424,6 +405,7 @@ struct TileInfo {
 };
 constexpr int kLast = 1;   // the CTA's last tile of the pair
 constexpr int kWhole = 2;  // the CTA has all tiles of the pair
+constexpr int kFirst = 4;  // the CTA's first tile of the pair
 __device__ __forceinline__ TileInfo read_info(uint32_t info, uint32_t i) {
     TileInfo v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -460,10 +442,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     grid_dep_launch();
 
     if (tid == 0) {
-        mbar_init(bar(L::B_QFULL), NLOAD / 32);
+        mbar_init(bar(L::B_QFULL), LOAD_WARPS);
         mbar_init(bar(L::B_QFREE), 1);
         for (int i = 0; i < L::NT * L::NS; i++) {
-            mbar_init(bar(L::B_UFULL + i), NLOAD / 32);  // step s of ring tile t: t NS + s
+            mbar_init(bar(L::B_UFULL + i), LOAD_WARPS);  // step s of ring tile t: t NS + s
             mbar_init(bar(L::B_UFREE + i), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -474,7 +456,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         }
         mbar_init(bar(L::B_OFULL), 1);
         mbar_init(bar(L::B_OFREE), NSOFT / 32);
-        for (int i = 0; i < NLOAD / 32; i++) mbar_init(bar(L::B_RAW + i), 1);
+        for (int i = 0; i < ROW_RING; i++) {
+            mbar_init(bar(L::B_RFULL + i), 1);
+            mbar_init(bar(L::B_RFREE + i), LOAD_WARPS);
+        }
         *abort = (base & 1023u) != 0;  // the swizzles want this alignment
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -740,106 +725,58 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         }
     } else if (warp < S_WARP) {
         // ------------------------------------------------ loads and dequantization
-        // A warp has eight rows of the tile. Per unit a row is 64 bytes of codes: four
-        // lanes of 16 bytes, eight rows per access (a lane per row would touch 32
-        // lines an access). The lanes' order gives each eight of a store's lanes
-        // four rows and two pieces: all banks.
+        // A warp has eight rows of the tile, two per thread. Per step a row is 128 bytes of codes, eight
+        // lanes of 16 bytes: four whole lines per access (with a lane per row an access
+        // touched 32, and the load pipe held up everything else). The lanes' order
+        // gives each eight of a store's lanes four rows and two pieces: all banks.
         const int lw = warp - NSOFT / 32;
-        const int piece = (lane & 1) | (lane >> 4) << 1;      // 32 channels of a unit
-        const int r = lw * 8 + ((lane >> 1) & 7);             // key row
-        // in a unit: the row, and the swizzled place of its piece i: swap ^ (i << 4)
+        const int piece = (lane & 1) | (lane >> 3) << 1;      // 32 channels of a step
+        const int r = lw * 8 + ((lane >> 1) & 3);             // key rows r and r + 4
+        // in a step: row r, and the swizzled place of its piece i: swap ^ (i << 4); row
+        // r + 4 lies 512 bytes on, and 64 swapped
         const uint32_t row_off = (piece >> 1) * CHUNK + (r >> 3) * 1024 + (r & 7) * 128;
         const uint32_t swap = (uint32_t)(((piece & 1) * 4) ^ (r & 7)) << 4;
+        const int row_bytes = a.C / 2, sf_bytes = a.C / (MX ? 32 : 16);
         bool ok = true;
         uint32_t seg = 0;
         Ring<L::NT> ur;
-        // Codes come by bulk copies of whole rows into this warp's eight of the raw
-        // buffer, issued by the lanes of piece 0 as soon as the last tile's codes are in
-        // registers: through the load pipe they cost as much as all else a tile does
-        // there (265 against 200 us for 8 x 128K).
-        const int row_bytes = a.C / 2, sf_bytes = a.C / (MX ? 32 : 16);
-        const uint32_t raw = base + L::RAW_OFF + r * L::RAW_PITCH, raw_bar = bar(L::B_RAW + lw);
-        auto copy_rows = [&](int64_t row) {
-            const uint32_t rows = __ballot_sync(0xffffffffu, row >= 0 && piece == 0);
-            if (lane == 0) mbar_expect_tx(raw_bar, __popc(rows) * row_bytes);
+        Ring<ROW_RING> rr;
+        uint4 code[L::NS][2];
+        uint32_t scl[L::NS][2];  // one E8M0 byte, or two E4M3; as loaded
+        auto load_tile = [&]() {
+            ok = wait_bar(bar(L::B_RFULL + rr.i), rr.phase, abort) && ok;
+            const volatile int64_t *rows = reinterpret_cast<const volatile int64_t *>(sm + L::ROW_OFF) + rr.i * TK + r;
+            const int64_t row[2] = {rows[0], rows[4]};
             __syncwarp();
-            if (row >= 0 && piece == 0) bulk_copy(raw, a.fp4 + row * row_bytes, row_bytes, raw_bar);
-        };
-        // Scales as loaded (anything done to them here would wait for the load). Wide:
-        // the four lanes of a row hold the scales of one unit each, eight or (MX) four
-        // bytes, and pass them round when that unit comes; one access per row and tile
-        // instead of one per row and unit. Otherwise: a lane's own, per unit.
-        const bool wide = a.wide_scales;
-        uint2 sw;
-        uint32_t scl[U];
-        auto load_scales = [&](int64_t row) {
-            const uint8_t *s = a.sf + row * sf_bytes;
-            sw = make_uint2(0, 0);
-            if (wide) {
-                if (row >= 0 && 128 * piece < a.C) {
-                    if constexpr (MX)
-                        sw.x = __ldg(reinterpret_cast<const uint32_t *>(s + 4 * piece));
-                    else
-                        sw = __ldg(reinterpret_cast<const uint2 *>(s + 8 * piece));
-                }
-            } else {
+            if (lane == 0) mbar_arrive(bar(L::B_RFREE + rr.i));
+            rr.next();
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int c0 = 128 * u + 32 * piece;
-                    scl[u] = 0;
-                    if (row >= 0 && c0 < a.C)
-                        scl[u] = MX ? (uint32_t)__ldg(s + c0 / 32)
-                                    : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s + c0 / 16));
+            for (int j = 0; j < 2; j++) {
+                const uint8_t *c = a.fp4 + row[j] * row_bytes + 16 * piece;
+                const uint8_t *s = a.sf + row[j] * sf_bytes + (MX ? piece : 2 * piece);
+#pragma unroll
+                for (int st = 0; st < L::NS; st++) {
+                    code[st][j] = make_uint4(0, 0, 0, 0);
+                    scl[st][j] = 0;
+                    if (ok && row[j] >= 0 && 256 * st + 32 * piece < a.C) {
+                        code[st][j] = ld_stream_v4(c + 128 * st);
+                        scl[st][j] = MX ? (uint32_t)__ldg(s + 8 * st)
+                                        : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s + 16 * st));
+                    }
                 }
             }
         };
-        // the lane's scales of unit u: one E8M0 byte, or two E4M3
-        auto scales = [&](int u) {
-            if (!wide) return scl[u];
-            const int from = (lane & 14) | (u & 1) | (u >> 1) << 4;  // the row's lane with piece u
-            const uint32_t x = __shfl_sync(0xffffffffu, sw.x, from);
-            if constexpr (MX) return (x >> (8 * piece)) & 0xFF;
-            const uint32_t y = __shfl_sync(0xffffffffu, sw.y, from);
-            return ((piece & 2 ? y : x) >> (16 * (piece & 1))) & 0xFFFF;
-        };
-        // A tile's table entries are read a tile before its rows. Whatever has to wait
-        // for a result stands before the loads go out: with six scoreboards a division
-        // behind them waits for them.
-        Walk ahead = w;
-        int32_t page;
-        int slot;
-        auto look_up = [&]() {
-            const int pos = ahead.position(r);
-            const int e = pos < 0 ? 0 : a.page_div(pos);
-            slot = pos - e * a.pk.page_size;
-            page = pos < 0 ? -1 : __ldg(a.pk.table + (int64_t)ahead.b * a.pk.max_pages + e);
-        };
-        auto find_row = [&]() {  // -1: no key
-            return page >= 0 && page < a.pk.n_pages ? (int64_t)page * a.pk.page_size + slot : (int64_t)-1;
-        };
-        look_up();
-        int64_t row = find_row(), row_next = -1;  // of this tile and of the next
-        copy_rows(row);
-        if (n_tiles > 1) {
-            ahead.next(a, true);
-            look_up();
-            row_next = find_row();
-        }
-        if (n_tiles > 2) {
-            ahead.next(a, true);
-            look_up();
-        }
-        load_scales(row);
-        bool first = true;
+        load_tile();
         for (int k = 0; k < n_tiles; k++) {
-            const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0);  // lanes 2 i (piece 0) hold rows i
-            if (first) {
+            const TileInfo info = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING);
+            const int keys = (info.flags >> 8) * 16;
+            if (info.flags & kFirst) {
                 // ---- queries of a new pair: one warp a head, lanes over channels
                 ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
                 float *qf = reinterpret_cast<float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH;
-                for (int h = lw; h < NH; h += NLOAD / 32) {
-                    const bool in = w.g * NH + h < a.Hq;
-                    const uint16_t *q = a.q + ((int64_t)w.b * a.Hq + w.g * NH + h) * a.C;
+                for (int h = lw; h < NH; h += LOAD_WARPS) {
+                    const bool in = info.g * NH + h < a.Hq;
+                    const uint16_t *q = a.q + ((int64_t)info.b * a.Hq + info.g * NH + h) * a.C;
                     uint4 v[(U + 1) / 2];
                     uint32_t top = 0;  // largest |q| as bf16 bits (NaN and inf above all others)
 #pragma unroll
@@ -882,53 +819,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(bar(L::B_QFULL));
                 seg++;
             }
-            first = w.tile + 1 == w.s.tiles;  // the next tile starts a pair
-            const int keys = w.keys16();
-            ok = wait_bar(raw_bar, k & 1, abort) && ok;
-            uint4 code[U];
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                code[u] = make_uint4(0, 0, 0, 0);
-                if (row >= 0) code[u] = ld_shared_v4(raw + 64 * u + 16 * piece);
-            }
-            fence_proxy_async();  // these reads before the next copies' writes
-            __syncwarp();
-            if (k + 1 < n_tiles) copy_rows(row_next);
 #pragma unroll
             for (int st = 0; st < L::NS; st++) {
                 ok = wait_bar(bar(L::B_UFREE + ur.i * L::NS + st), ur.phase ^ 1, abort) && ok;
-                if (st == 0 && lane == 0) {
-                    const uint32_t vi = (uint32_t)k % VALID_RING;
-                    uint32_t bits = seen & 0x5555u;  // every other bit, drawn together
-                    bits = (bits | bits >> 1) & 0x3333u;
-                    bits = (bits | bits >> 2) & 0x0F0Fu;
-                    bits |= bits >> 4;
-                    reinterpret_cast<volatile uint8_t *>(sm + L::VALID_OFF)[vi * 8 + lw] = (uint8_t)bits;
-                    if (lw == 0) {
-                        const bool from_start = w.tile <= k;  // the pair's first tile is this CTA's too
-                        const bool last = first || k + 1 == n_tiles;
-                        const int flags = (last ? kLast : 0) | (first && from_start ? kWhole : 0) | (keys / 16) << 8;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + L::INFO_OFF + 16 * vi),
-                                     "r"(w.b), "r"(w.g), "r"(flags), "r"(2 * cta + (w.tile < k ? 1 : 0))
-                                     : "memory");
-                    }
-                }
+                if (8 * lw < keys && 256 * st + 32 * piece < a.C) {
+                    const uint32_t dst = base + L::K_OFF + (ur.i * U + 2 * st) * UNIT + row_off;
 #pragma unroll
-                for (int u = 2 * st; u < 2 * st + 2 && u < U; u++) {
-                    const uint32_t sc = scales(u);
-                    if (8 * lw < keys && 128 * u + 32 * piece < a.C) {
-                        const uint32_t dst = base + L::K_OFF + (ur.i * U + u) * UNIT + row_off;
-                        const uint32_t wd[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+                    for (int j = 0; j < 2; j++) {
+                        const uint32_t wd[4] = {code[st][j].x, code[st][j].y, code[st][j].z, code[st][j].w};
                         if constexpr (MX) {
-                            const MxScale s = mx_scale(sc);
+                            const MxScale s = mx_scale(scl[st][j]);
 #pragma unroll
-                            for (int i = 0; i < 4; i++) st_shared_v4(dst + (swap ^ (i << 4)), rows_bf16(wd[i], s));
+                            for (int i = 0; i < 4; i++)
+                                st_shared_v4(dst + 512 * j + (swap ^ ((i + 4 * j) << 4)), rows_bf16(wd[i], s));
                         } else {
                             uint32_t s01;  // the two groups' scales in f16
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s01) : "h"((uint16_t)sc));
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s01) : "h"((uint16_t)scl[st][j]));
                             const uint32_t s[2] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232)};
 #pragma unroll
-                            for (int i = 0; i < 4; i++) st_shared_v4(dst + (swap ^ (i << 4)), rows_f16(wd[i], s[i >> 1]));
+                            for (int i = 0; i < 4; i++)
+                                st_shared_v4(dst + 512 * j + (swap ^ ((i + 4 * j) << 4)), rows_f16(wd[i], s[i >> 1]));
                         }
                     }
                 }
@@ -937,14 +847,58 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(bar(L::B_UFULL + ur.i * L::NS + st));
             }
             ur.next();
-            row = row_next;
-            row_next = k + 2 < n_tiles ? find_row() : -1;
-            if (k + 3 < n_tiles) {
+            // after this tile's last fence, which would wait for them
+            if (k + 1 < n_tiles) load_tile();
+        }
+    } else if (warp == SCOUT_WARP) {
+        // ------------------------------------------------ the scout: where the rows of the
+        // coming tiles lie, which keys there are, and what the tile is. Table entries are
+        // looked at one tile after they were asked for.
+        bool ok = true;
+        Ring<ROW_RING> rr;
+        Walk ahead = w;
+        int32_t page[2];
+        int slot[2];
+        auto look_up = [&]() {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int pos = ahead.position(lane + 32 * j);
+                const int e = pos < 0 ? 0 : a.page_div(pos);
+                slot[j] = pos - e * a.pk.page_size;
+                page[j] = pos < 0 ? -1 : __ldg(a.pk.table + (int64_t)ahead.b * a.pk.max_pages + e);
+            }
+        };
+        look_up();
+        for (int k = 0; k < n_tiles && ok; k++) {
+            int64_t row[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                row[j] = page[j] >= 0 && page[j] < a.pk.n_pages ? (int64_t)page[j] * a.pk.page_size + slot[j] : -1;
+            if (k + 1 < n_tiles) {
                 ahead.next(a, true);
                 look_up();
             }
-            // after this tile's last fence, which would wait for them
-            if (k + 1 < n_tiles) load_scales(row);
+            const uint32_t lo = __ballot_sync(0xffffffffu, row[0] >= 0), hi = __ballot_sync(0xffffffffu, row[1] >= 0);
+            ok = wait_bar(bar(L::B_RFREE + rr.i), rr.phase ^ 1, abort) && ok;
+            volatile int64_t *to = reinterpret_cast<volatile int64_t *>(sm + L::ROW_OFF) + rr.i * TK;
+            to[lane] = row[0];
+            to[lane + 32] = row[1];
+            if (lane == 0) {
+                const uint32_t vi = (uint32_t)k % VALID_RING;
+                volatile uint32_t *v = reinterpret_cast<volatile uint32_t *>(sm + L::VALID_OFF) + 2 * vi;
+                v[0] = lo;
+                v[1] = hi;
+                const bool end_seq = w.tile + 1 == w.s.tiles;
+                const bool from_start = w.tile <= k;  // the pair's first tile is this CTA's too
+                const int flags = (end_seq || k + 1 == n_tiles ? kLast : 0) | (end_seq && from_start ? kWhole : 0) |
+                                  (k == 0 || w.tile == 0 ? kFirst : 0) | (w.keys16() / 16) << 8;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + L::INFO_OFF + 16 * vi), "r"(w.b),
+                             "r"(w.g), "r"(flags), "r"(2 * cta + (w.tile < k ? 1 : 0))
+                             : "memory");
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::B_RFULL + rr.i));
+            rr.next();
             w.next(a, k + 1 < n_tiles);
         }
     } else if (warp == S_WARP) {

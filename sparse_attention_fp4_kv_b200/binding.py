@@ -9,6 +9,7 @@ Importing this module loads the library and raises if it is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, Optional, Sequence
 
@@ -346,15 +347,26 @@ class DecodeStack:
 ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
 
 
+# These calls are a few microseconds each on the device, so the marshalling counts:
+# raw pointers and stream handles go to ctypes as plain integers.
 def _here(stream, *tensors):
-    """The paged calls launch on the stream's device (the current one without a
-    stream) and refuse tensors of another."""
-    dev = torch.cuda.current_device() if stream is None else stream.device.index
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the stream is on device {dev}, the current device is another")
+    """The stream handle of a paged call. It launches on the stream's device, which has
+    to be the current one, and refuses tensors of another."""
+    dev = torch.cuda.current_device()
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the current device is {dev}")
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the call runs on device {dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libcsa2 must be contiguous")
+    return t.data_ptr()
 
 
 def _scratch(nbytes: int, like, stream):
@@ -371,10 +383,10 @@ def csa2_rope_freqs(inv_freq, theta: float = 10000.0, scaling: int = ROPE_PLAIN,
                     stream=None) -> None:
     """inv_freq [rot_dim / 2] fp64: the table csa2_rope reads."""
     _want(inv_freq, torch.float64, "inv_freq")
-    _here(stream, inv_freq)
+    st = _here(stream, inv_freq)
     _check("csa2_rope_freqs", lib.csa2_rope_freqs(
         2 * inv_freq.numel(), float(theta), scaling, float(factor), orig_ctx, float(beta_fast),
-        float(beta_slow), _ptr(inv_freq), _stream(stream)))
+        float(beta_slow), _addr(inv_freq), st))
 
 
 def csa2_rope(x, pos, inv_freq, out, rot_start: int = 0, interleaved: bool = True,
@@ -392,11 +404,11 @@ def csa2_rope(x, pos, inv_freq, out, rot_start: int = 0, interleaved: bool = Tru
     assert out.shape == x.shape and pos.shape == (T,) and inv_freq.dim() == 1
     if D > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
         raise ValueError("the channels of x and out must be contiguous")
-    _here(stream, x, out, pos, inv_freq)
+    st = _here(stream, x, out, pos, inv_freq)
     _check("csa2_rope", lib.csa2_rope(
-        _P(x.data_ptr()), _P(out.data_ptr()), int(x.dtype == torch.float32), _ptr(pos), _ptr(inv_freq),
+        x.data_ptr(), out.data_ptr(), int(x.dtype == torch.float32), _addr(pos), _addr(inv_freq),
         T, H, D, rot_start, 2 * inv_freq.shape[0], 0 if interleaved else 1, int(inverse),
-        float(mscale), x.stride(0), x.stride(1), out.stride(0), out.stride(1), _stream(stream)))
+        float(mscale), x.stride(0), x.stride(1), out.stride(0), out.stride(1), st))
 
 
 def _pool(kv_fp4, kv_sf, C: int, mx: bool):
@@ -423,11 +435,11 @@ def csa2_paged_kv_append_fp4(kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_va
     if n_valid is not None:
         _want(n_valid, torch.int32, "n_valid")
         assert n_valid.shape == (B,)
-    _here(stream, kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    st = _here(stream, kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid)
     name = "csa2_paged_kv_append_mxfp4" if mx else "csa2_paged_kv_append_fp4"
     _check(name, getattr(lib, name)(
-        _ptr(kv_bf16), B, n, C, _ptr(start_pos), _ptr(n_valid), _ptr(page_table), page_table.shape[1],
-        page_size, n_pages, _ptr(kv_fp4), _ptr(kv_sf), _stream(stream)))
+        _addr(kv_bf16), B, n, C, _addr(start_pos), _addr(n_valid), _addr(page_table), page_table.shape[1],
+        page_size, n_pages, _addr(kv_fp4), _addr(kv_sf), st))
 
 
 def csa2_paged_kv_gather(kv_fp4, kv_sf, page_table, start_pos, out, n_valid=None, stream=None,
@@ -443,13 +455,14 @@ def csa2_paged_kv_gather(kv_fp4, kv_sf, page_table, start_pos, out, n_valid=None
     if n_valid is not None:
         _want(n_valid, torch.int32, "n_valid")
         assert n_valid.shape == (B,)
-    _here(stream, out, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    st = _here(stream, out, start_pos, page_table, kv_fp4, kv_sf, n_valid)
     name = "csa2_paged_kv_gather_mxfp4" if mx else "csa2_paged_kv_gather_fp4"
     _check(name, getattr(lib, name)(
-        _ptr(kv_fp4), _ptr(kv_sf), _ptr(page_table), page_table.shape[1], page_size, n_pages,
-        _ptr(start_pos), _ptr(n_valid), B, n, C, _ptr(out), _stream(stream)))
+        _addr(kv_fp4), _addr(kv_sf), _addr(page_table), page_table.shape[1], page_size, n_pages,
+        _addr(start_pos), _addr(n_valid), B, n, C, _addr(out), st))
 
 
+@functools.lru_cache(maxsize=256)
 def pages_workspace_size(n_pages: int, n: int = 0) -> int:
     return lib.csa2_pages_workspace_size(n_pages, n)
 
@@ -474,11 +487,11 @@ def csa2_pages_extend(page_table, ref, want_len, page_size: int, n_failed, ws=No
     _want(n_failed, torch.int32, "n_failed")
     S, M = page_table.shape
     assert want_len.shape == (S,)
-    _here(stream, page_table, ref, want_len, n_failed, ws)
+    st = _here(stream, page_table, ref, want_len, n_failed, ws)
     ws, wsb = _pages_ws(ws, ref.shape[0], S, ref, stream)
     _check("csa2_pages_extend", lib.csa2_pages_extend(
-        _ptr(page_table), S, M, _ptr(ref), ref.shape[0], page_size, _ptr(want_len), _ptr(n_failed),
-        _ptr(ws), wsb, _stream(stream)))
+        _addr(page_table), S, M, _addr(ref), ref.shape[0], page_size, _addr(want_len), _addr(n_failed),
+        _addr(ws), wsb, st))
 
 
 def csa2_pages_fork(page_table, ref, seq_len, src, dst, page_size: int, pairs, n_failed, ws=None,
@@ -491,11 +504,11 @@ def csa2_pages_fork(page_table, ref, seq_len, src, dst, page_size: int, pairs, n
     S, M = page_table.shape
     F = src.shape[0]
     assert seq_len.shape == (S,) and dst.shape == (F,) and pairs.shape == (F, 2)
-    _here(stream, page_table, ref, seq_len, src, dst, pairs, n_failed, ws)
+    st = _here(stream, page_table, ref, seq_len, src, dst, pairs, n_failed, ws)
     ws, wsb = _pages_ws(ws, ref.shape[0], F, ref, stream)
     _check("csa2_pages_fork", lib.csa2_pages_fork(
-        _ptr(page_table), S, M, _ptr(ref), ref.shape[0], page_size, _ptr(seq_len), _ptr(src), _ptr(dst), F,
-        _ptr(pairs), _ptr(n_failed), _ptr(ws), wsb, _stream(stream)))
+        _addr(page_table), S, M, _addr(ref), ref.shape[0], page_size, _addr(seq_len), _addr(src), _addr(dst), F,
+        _addr(pairs), _addr(n_failed), _addr(ws), wsb, st))
 
 
 def csa2_pages_free(page_table, ref, seq, page_size: int, keep_len=None, stream=None) -> None:
@@ -506,20 +519,21 @@ def csa2_pages_free(page_table, ref, seq, page_size: int, keep_len=None, stream=
     if keep_len is not None:
         _want(keep_len, torch.int64, "keep_len")
         assert keep_len.shape == (F,)
-    _here(stream, page_table, ref, seq, keep_len)
+    st = _here(stream, page_table, ref, seq, keep_len)
     _check("csa2_pages_free", lib.csa2_pages_free(
-        _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(ref), ref.shape[0], page_size,
-        _ptr(seq), _ptr(keep_len), F, _stream(stream)))
+        _addr(page_table), page_table.shape[0], page_table.shape[1], _addr(ref), ref.shape[0], page_size,
+        _addr(seq), _addr(keep_len), F, st))
 
 
 def _page_bufs(bufs, n_pages: int):
     """Tensors [n_pages][...] of one cache -> the C array of their bases and page sizes."""
     arr = (csa2_page_buf * max(1, len(bufs)))()
-    for i, t in enumerate(bufs):
+    for a, t in zip(arr, bufs):
         if not t.is_cuda:
             raise ValueError("the cache buffers must be CUDA tensors")
         assert t.shape[0] == n_pages
-        arr[i] = csa2_page_buf(_ptr(t), t[0].numel() * t.element_size())
+        a.base = _addr(t)
+        a.page_bytes = t.numel() // n_pages * t.element_size()
     return arr
 
 
@@ -529,9 +543,9 @@ def csa2_pages_copy(pairs, bufs: Sequence[torch.Tensor], stream=None) -> None:
     F = pairs.shape[0]
     assert pairs.shape == (F, 2) and len(bufs) >= 1
     n_pages = bufs[0].shape[0]
-    _here(stream, pairs, *bufs)
+    st = _here(stream, pairs, *bufs)
     _check("csa2_pages_copy", lib.csa2_pages_copy(
-        _ptr(pairs), F, _page_bufs(bufs, n_pages), len(bufs), n_pages, _stream(stream)))
+        _addr(pairs), F, _page_bufs(bufs, n_pages), len(bufs), n_pages, st))
 
 
 def csa2_pages_compact(page_table, ref, bufs: Sequence[torch.Tensor], page_table_out, ref_out, n_live,
@@ -543,12 +557,17 @@ def csa2_pages_compact(page_table, ref, bufs: Sequence[torch.Tensor], page_table
     _want_pages(page_table_out, ref_out)
     _want(n_live, torch.int32, "n_live")
     assert page_table_out.shape == page_table.shape and ref_out.shape == ref.shape
-    _here(stream, page_table, ref, page_table_out, ref_out, n_live, ws, *bufs)
+    st = _here(stream, page_table, ref, page_table_out, ref_out, n_live, ws, *bufs)
     ws, wsb = _pages_ws(ws, ref.shape[0], 0, ref, stream)
     _check("csa2_pages_compact", lib.csa2_pages_compact(
-        _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(ref), ref.shape[0],
-        _page_bufs(bufs, ref.shape[0]), len(bufs), _ptr(page_table_out), _ptr(ref_out), _ptr(n_live),
-        _ptr(ws), wsb, _stream(stream)))
+        _addr(page_table), page_table.shape[0], page_table.shape[1], _addr(ref), ref.shape[0],
+        _page_bufs(bufs, ref.shape[0]), len(bufs), _addr(page_table_out), _addr(ref_out), _addr(n_live),
+        _addr(ws), wsb, st))
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_attn_ws(device: int, B: int, Hq: int, C: int) -> int:
+    return lib.csa2_paged_attn_workspace_size(B, Hq, C)
 
 
 def paged_attn_workspace_size(B: int, Hq: int, C: int) -> int:
@@ -571,11 +590,11 @@ def csa2_paged_attn_decode(q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, soft
     if lse is not None:
         _want(lse, torch.float32, "lse")
         assert lse.shape == (B, Hq)
-    _here(stream, q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, lse, ws)
+    st = _here(stream, q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, lse, ws)
     if ws is None:
-        ws = _scratch(paged_attn_workspace_size(B, Hq, C), q_bf16, stream)
+        ws = _scratch(_paged_attn_ws(q_bf16.get_device(), B, Hq, C), q_bf16, stream)
     name = "csa2_paged_attn_decode_mxfp4" if mx else "csa2_paged_attn_decode"
     _check(name, getattr(lib, name)(
-        _ptr(q_bf16), _ptr(kv_fp4), _ptr(kv_sf), _ptr(page_table), page_table.shape[1], page_size,
-        n_pages, _ptr(ctx_len), n_win, n_sink, B, Hq, C, float(softmax_scale), _ptr(out), _ptr(lse),
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _addr(q_bf16), _addr(kv_fp4), _addr(kv_sf), _addr(page_table), page_table.shape[1], page_size,
+        n_pages, _addr(ctx_len), n_win, n_sink, B, Hq, C, float(softmax_scale), _addr(out), _addr(lse),
+        _addr(ws), ws.numel() * ws.element_size(), st))

@@ -11,94 +11,103 @@ int pa::launch_paged_attn_fp4(const Args &a, int nh, int G, cudaStream_t s) { re
 namespace pa {
 
 // Joins the parts that the CTAs of a split (sequence, head group) pair left:
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. Block (pair, y) takes
-// `per` heads; its threads are columns of four channels times groups of parts, so
-// that many parts' loads are in flight. Pairs without a key get zeros here, pairs
-// within one CTA are already finished. Block (0, 0) also sets the error word.
-constexpr int JT = 512;
-constexpr int MAX_PARTS = 1024;  // CTAs of the attention kernel
-__global__ void __launch_bounds__(JT) join_kernel(const Args a, int NH, int pitch, int G, int per, int *err) {
-    __shared__ float weight[MAX_PARTS];
-    __shared__ float4 acc[JT];
-    __shared__ float red[2][JT / 32];
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. A warp takes 128 channels of
+// one head, four per lane, and 32 parts at a time: lane i reads part i's (m, l),
+// the weights go round by shuffles, eight parts' O are in flight. WIDE: the eight
+// warps of a block share one such piece of work and take parts in turn, for the few
+// pairs of a small batch, which are split over many CTAs; else each has its own.
+// Pairs without a key get zeros here, pairs within one CTA are already finished.
+// Block 0 also sets the error word.
+constexpr int JW = 8;            // warps
+constexpr int MAX_CTAS = 1024;   // of the attention kernel
+template <bool WIDE>
+__global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int pitch, int G, int chunks, int work, int *err) {
+    __shared__ float4 acc_s[JW][32];
+    __shared__ float2 ml_s[JW];
     grid_dep_wait();
-    const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) {
         int any = 0;
-        for (int i = tid; i < G; i += JT) any |= a.flags[i];
+        for (int i = threadIdx.x; i < G; i += JW * 32) any |= a.flags[i];
         any = __syncthreads_or(any);
-        if (tid == 0) *err = any != 0;
+        if (threadIdx.x == 0) *err = any != 0;
     }
-    const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+    // work item: (pair, head of the group, chunk of 128 channels)
+    const int item = WIDE ? blockIdx.x : blockIdx.x * JW + warp;
+    if (item >= work) return;
+    const int chunk = item % chunks, hh = item / chunks % NH, pair = item / chunks / NH;
+    const int b = pair / a.groups, g = pair % a.groups, h = g * NH + hh, c = 128 * chunk + 4 * lane;
+    if (h >= a.Hq) return;
     const int64_t T = a.prefix[a.B] * a.groups, p0 = a.prefix[b], tiles = a.prefix[b + 1] - p0;
+    uint2 *out = reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.Hq + h) * a.C + c);
+    float *lse = a.lse && chunk == 0 && lane == 0 ? a.lse + (int64_t)b * a.Hq + h : nullptr;
+    if (tiles == 0) {
+        if ((!WIDE || warp == 0) && c < a.C) *out = make_uint2(0, 0);
+        if ((!WIDE || warp == 0) && lse) *lse = -INFINITY;
+        return;
+    }
     const int64_t t0 = p0 * a.groups + g * tiles;
     const int sharers = sharing(T, G);
-    const int lo = tiles ? owner_of(t0, T, sharers) : 0, hi = tiles ? owner_of(t0 + tiles - 1, T, sharers) : 0;
-    if (tiles && lo == hi) return;
+    const int lo = owner_of(t0, T, sharers), hi = owner_of(t0 + tiles - 1, T, sharers);
+    if (lo == hi) return;
     const int n = hi - lo + 1;
     // the part of the first CTA: its second segment unless its share starts here
-    const int slot0 = 2 * lo + (tiles && share_begin(lo, T, sharers) != t0 ? 1 : 0);
+    const int slot0 = 2 * lo + (share_begin(lo, T, sharers) != t0 ? 1 : 0);
     auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (lo + i); };
-    const int cols = a.C / 4, col = tid % cols, grp = tid / cols, groups = JT / cols;
-    for (int y = 0; y < per; y++) {
-        const int hh = blockIdx.y * per + y, h = g * NH + hh;
-        if (hh >= NH || h >= a.Hq) break;
-        uint2 *out = reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.Hq + h) * a.C);
-        float *lse = a.lse ? a.lse + (int64_t)b * a.Hq + h : nullptr;
-        if (!tiles) {
-            if (tid < cols) out[tid] = make_uint2(0, 0);
-            if (tid == 0 && lse) *lse = -INFINITY;
-            continue;
-        }
-        float m = REF_NONE;
-        for (int i = tid; i < n; i += JT) m = fmaxf(m, a.part_ml[((int64_t)slot(i) * NH + hh) * 2]);
+    float m = REF_NONE, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int step = WIDE ? JW : 1, first = WIDE ? warp : 0;  // this warp's parts: first, first + step, ...
+    for (int i0 = first; i0 < n; i0 += 32 * step) {
+        const int mine = i0 + lane * step;
+        float2 ml = make_float2(REF_NONE, 0.0f);
+        if (mine < n) ml = *reinterpret_cast<const float2 *>(a.part_ml + ((int64_t)slot(mine) * NH + hh) * 2);
+        float top = fmaxf(m, ml.x);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if ((tid & 31) == 0) red[0][tid >> 5] = m;
-        __syncthreads();
-        for (int i = 0; i < JT / 32; i++) m = fmaxf(m, red[0][i]);
-        float sum = 0.0f;
-        for (int i = tid; i < n; i += JT) {
-            const float *ml = a.part_ml + ((int64_t)slot(i) * NH + hh) * 2;
-            const float wt = ex2(ml[0] - m);
-            weight[i] = wt;
-            sum += wt * ml[1];
-        }
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float old = ex2(m - top), wt = ex2(ml.x - top);
+        float sum = wt * ml.y;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if ((tid & 31) == 0) red[1][tid >> 5] = sum;
-        __syncthreads();
-        sum = 0.0f;
-        for (int i = 0; i < JT / 32; i++) sum += red[1][i];
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (grp < groups) {
-            const float *o = a.part_o + (int64_t)hh * pitch + 4 * col;
+        l = l * old + sum;
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+        m = top;
+        const int count = (n - i0 + step - 1) / step < 32 ? (n - i0 + step - 1) / step : 32;
+        const float *po = a.part_o + (int64_t)hh * pitch + c;
 #pragma unroll 8
-            for (int i = grp; i < n; i += groups) {
-                const float4 x = *reinterpret_cast<const float4 *>(o + (int64_t)slot(i) * NH * pitch);
-                const float wt = weight[i];
-                v.x += wt * x.x;
-                v.y += wt * x.y;
-                v.z += wt * x.z;
-                v.w += wt * x.w;
-            }
+        for (int j = 0; j < count; j++) {
+            const float w = __shfl_sync(0xffffffffu, wt, j);
+            const float4 x = *reinterpret_cast<const float4 *>(po + (int64_t)slot(i0 + j * step) * NH * pitch);
+            o.x += w * x.x;
+            o.y += w * x.y;
+            o.z += w * x.z;
+            o.w += w * x.w;
         }
-        acc[tid] = v;
-        __syncthreads();
-        if (tid < cols) {
-            for (int i = 1; i < groups; i++) {
-                const float4 x = acc[i * cols + tid];
-                v.x += x.x;
-                v.y += x.y;
-                v.z += x.z;
-                v.w += x.w;
-            }
-            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-            out[tid] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-        }
-        if (tid == 0 && lse) *lse = sum != 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
-        __syncthreads();
     }
+    if constexpr (WIDE) {
+        acc_s[warp][lane] = o;
+        if (lane == 0) ml_s[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp > 0) return;
+        float top = ml_s[0].x;
+#pragma unroll
+        for (int i = 1; i < JW; i++) top = fmaxf(top, ml_s[i].x);
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < JW; i++) {
+            const float w = ex2(ml_s[i].x - top);
+            const float4 x = acc_s[i][lane];
+            l += w * ml_s[i].y;
+            o.x += w * x.x;
+            o.y += w * x.y;
+            o.z += w * x.z;
+            o.w += w * x.w;
+        }
+        m = top;
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if (c < a.C) *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lse) *lse = l != 0.0f ? (m + log2f(l)) * LN2 : -INFINITY;
 }
 
 // Heads of one group: the smallest MMA width that holds them, 64 at most.
@@ -135,7 +144,7 @@ Ws layout(void *base, int B, int Hq, int C, int G) {
 // One CTA per SM: the shared memory of one leaves no room for a second.
 int grid_ctas() {
     const int n = num_sms();
-    return n < MAX_PARTS ? n : MAX_PARTS;
+    return n < MAX_CTAS ? n : MAX_CTAS;
 }
 
 int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_pages,
@@ -151,22 +160,25 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
     if (!aligned(q, 16) || !aligned(fp4, 16) || !aligned(out, 8) || (!mx && !aligned(sf, 4))) return CSA2_ERR_ALIGN;
     if (B == 0) return CSA2_OK;
     const int G = grid_ctas(), nh = group_heads(Hq), groups = (Hq + nh - 1) / nh;
-    if ((int64_t)B * groups > INT32_MAX) return CSA2_ERR_SHAPE;
+    const int pitch = (C + 127) / 128 * 128, chunks = pitch / 128;
+    const int64_t work = (int64_t)B * groups * nh * chunks;
+    if (work > INT32_MAX) return CSA2_ERR_SHAPE;
     const Ws w = layout(ws, B, Hq, C, G);
     if (!ws || ws_bytes < w.bytes) return CSA2_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return CSA2_ERR_ALIGN;
     cudaStream_t s = (cudaStream_t)stream;
     const Args a{(const uint16_t *)q, fp4, sf, PagedKv{table, max_pages, page_size, n_pages}, ctx_len,
-                 (int)(n_win < cap ? n_win : cap), (int)(n_sink < cap ? n_sink : cap), (int)cap, fast_div(page_size), B, Hq, C, groups, scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml, w.o};
+                 (int)(n_win < cap ? n_win : cap), (int)(n_sink < cap ? n_sink : cap), (int)cap,
+                 fast_div(page_size), B, Hq, C, groups, scale, (uint16_t *)out, lse, w.flags, w.prefix, w.ml,
+                 w.o};
     const int st = mx ? launch_paged_attn_mxfp4(a, nh, G, s) : launch_paged_attn_fp4(a, nh, G, s);
     if (st != CSA2_OK) return st;
-    // one head per block until there are a few blocks per SM
-    const int pairs = B * groups;
-    int blocks = 4 * G / pairs;
-    blocks = blocks < 1 ? 1 : blocks > nh ? nh : blocks;
-    const int per = (nh + blocks - 1) / blocks;
-    return launch_kernel(true, join_kernel, dim3((unsigned)pairs, (unsigned)((nh + per - 1) / per)), dim3(JT), 0,
-                         s, a, nh, (C + 127) / 128 * 128, G, per, w.err);
+    // a block per piece of work while that leaves the SMs a few blocks each
+    if (work <= 16 * G)
+        return launch_kernel(true, join_kernel<true>, dim3((unsigned)work), dim3(JW * 32), 0, s, a, nh, pitch, G, chunks,
+                             (int)work, w.err);
+    return launch_kernel(true, join_kernel<false>, dim3((unsigned)((work + JW - 1) / JW)), dim3(JW * 32), 0, s, a, nh,
+                         pitch, G, chunks, (int)work, w.err);
 }
 
 }  // namespace pa

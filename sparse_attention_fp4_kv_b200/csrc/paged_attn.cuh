@@ -6,23 +6,34 @@
 // with K = V = the dequantized rows. Keys and channels lie on the MMAs' 128 rows
 // because a decode query has 64 heads or fewer, and M = 64 runs at half rate.
 //
-// Work: every sequence is cut into tiles of 128 visible keys; the tiles of all
+// Work: every sequence is cut into tiles of 64 visible keys; the tiles of all
 // (sequence, head group) pairs form one list that is divided evenly over the
 // CTAs (one per SM), so that one long sequence and many short ones both fill the
 // card. A CTA walks its share with an online softmax and keeps O^T in tensor
 // memory; a pair that lies within one CTA is finished there, otherwise each CTA
 // leaves (m, l, O) of its part and the combine kernel joins them.
 //
-// Roles of the 17 warps:
-//   0-7   softmax: thread = key; warps 0-3 the first half of the heads, 4-7 the
-//         second. Also the epilogue.
-//   8-15  loads: codes and scales of the next tile in registers while the
-//         current one is dequantized to shared memory; the queries.
-//   16    one thread issues the MMAs, first P V of a tile whose weights are
-//         ready, else S of the next.
-// Shared memory holds a ring of units of 128 keys x 128 channels (32 KB); a
-// tile of C channels is ceil(C / 128) units, each read by S as K (K-major) and by
-// O as V (MN-major) from the same bytes.
+// Roles of the 19 warps:
+//   0-7   softmax: thread = a key and a quarter of the heads; warps 0-3 the first
+//         half of the heads, 4-7 the second. Also the epilogue.
+//   8-15  loads: codes and scales of the next tile in registers while the current
+//         one is dequantized to shared memory; the queries.
+//   16    issues S, 17 issues P V: each waits, suspended, for its own barriers.
+//   18    the scout: page table entries, rows, and what the coming tiles are.
+// Shared memory holds a ring of tiles, each ceil(C / 128) units of 64 keys x 128
+// channels (16 KB), read by S as K (K-major) and by O as V (MN-major) from the same
+// bytes. A tile is handed over in steps of two units, both ways.
+//
+// Bound (8 sequences of 128K, 64 heads, 512 channels): 137 GFLOP, 84 us at the
+// measured bf16 rate; 303 MB, 46 us. M = 64 and N = 64 leave the MMAs at half of
+// that rate at best (an MMA of 64 x 64 x 16 takes 35 cycles, one of 128 x 64 x 16
+// 50), and they share shared memory with 64 KB of dequantized rows per tile.
+// Measured steps: one thread polling two barriers 585 us (128-key tiles, one in
+// the ring), rows read whole lines at a time and a warp that stays together 280, two
+// issuing warps and bulk copies 268, the scout, which takes the walk and the
+// table out of the load warps, 238, loads past L1 229. 128-key tiles
+// (M = 128 for S) leave room for one tile: 292. 16 load warps, at 72
+// registers, spill: 342.
 //
 // Softmax: out = sum 2^(x_j - r) v_j / sum 2^(x_j - r) for any reference r. r is
 // the head's maximum of its first tile and moves only when a score exceeds it
@@ -774,44 +785,54 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                 // ---- queries of a new pair: one warp a head, lanes over channels
                 ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
                 float *qf = reinterpret_cast<float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH;
-                for (int h = lw; h < NH; h += LOAD_WARPS) {
-                    const bool in = info.g * NH + h < a.Hq;
-                    const uint16_t *q = a.q + ((int64_t)info.b * a.Hq + info.g * NH + h) * a.C;
-                    uint4 v[(U + 1) / 2];
-                    uint32_t top = 0;  // largest |q| as bf16 bits (NaN and inf above all others)
+                constexpr int MINE = NH / LOAD_WARPS, HB = U > 2 || MINE < 4 ? 2 : 4;  // heads of a warp, and at a time
+#pragma unroll 1
+                for (int h0 = 0; h0 < MINE; h0 += HB) {
+                    uint4 v[HB][(U + 1) / 2];  // all loads before the first use
 #pragma unroll
-                    for (int i = 0; i < (U + 1) / 2; i++) {
-                        const int c = 256 * i + 8 * lane;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (in && c < a.C) v[i] = __ldg(reinterpret_cast<const uint4 *>(q + c));
-                        const uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    for (int j = 0; j < HB; j++) {
+                        const int h = info.g * NH + (h0 + j) * LOAD_WARPS + lw;
+                        const uint16_t *q = a.q + ((int64_t)info.b * a.Hq + h) * a.C;
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t lo = u4[j] & 0x7FFF, hi = (u4[j] >> 16) & 0x7FFF;
-                            top = max(top, max(lo, hi));
+                        for (int i = 0; i < (U + 1) / 2; i++) {
+                            const int c = 256 * i + 8 * lane;
+                            v[j][i] = make_uint4(0, 0, 0, 0);
+                            if (h < a.Hq && c < a.C) v[j][i] = __ldg(reinterpret_cast<const uint4 *>(q + c));
                         }
                     }
-                    float mul = 1.0f, f = a.scale * LOG2E;
-                    if constexpr (!MX) {
-                        top = __reduce_max_sync(0xffffffffu, top);
-                        // 2^e with the top exponent brought to 13; e <= 100 keeps 2^e in range
-                        int e = 13 - ((int)(top >> 7) - 127);
-                        e = e > 100 ? 100 : e;
-                        mul = __uint_as_float((uint32_t)(e + 127) << 23);
-                        f *= __uint_as_float((uint32_t)(127 - e) << 23);
-                    }
-                    if (lane == 0) qf[h] = f;
 #pragma unroll
-                    for (int i = 0; i < (U + 1) / 2; i++) {
-                        const int c = 256 * i + 8 * lane;
-                        if (c >= 128 * U) continue;
-                        uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    for (int j = 0; j < HB; j++) {
+                        const int h = (h0 + j) * LOAD_WARPS + lw;
+                        float mul = 1.0f, f = a.scale * LOG2E;
                         if constexpr (!MX) {
+                            uint32_t top = 0;  // largest |q| as bf16 bits (NaN and inf above all others)
 #pragma unroll
-                            for (int j = 0; j < 4; j++) u4[j] = pack_f16x2(bf16_lo(u4[j]) * mul, bf16_hi(u4[j]) * mul);
+                            for (int i = 0; i < (U + 1) / 2; i++) {
+                                const uint32_t u4[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
+#pragma unroll
+                                for (int e = 0; e < 4; e++) top = max(top, max(u4[e] & 0x7FFF, (u4[e] >> 16) & 0x7FFF));
+                            }
+                            top = __reduce_max_sync(0xffffffffu, top);
+                            // 2^e with the top exponent brought to 13; e <= 100 keeps 2^e in range
+                            int e = 13 - ((int)(top >> 7) - 127);
+                            e = e > 100 ? 100 : e;
+                            mul = __uint_as_float((uint32_t)(e + 127) << 23);
+                            f *= __uint_as_float((uint32_t)(127 - e) << 23);
                         }
-                        st_shared_v4(base + L::Q_OFF + (c >> 6) * L::Q_CHUNK + sw128(h, (c >> 3) & 7),
-                                     make_uint4(u4[0], u4[1], u4[2], u4[3]));
+                        if (lane == 0) qf[h] = f;
+#pragma unroll
+                        for (int i = 0; i < (U + 1) / 2; i++) {
+                            const int c = 256 * i + 8 * lane;
+                            if (c >= 128 * U) continue;
+                            uint32_t u4[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
+                            if constexpr (!MX) {
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    u4[e] = pack_f16x2(bf16_lo(u4[e]) * mul, bf16_hi(u4[e]) * mul);
+                            }
+                            st_shared_v4(base + L::Q_OFF + (c >> 6) * L::Q_CHUNK + sw128(h, (c >> 3) & 7),
+                                         make_uint4(u4[0], u4[1], u4[2], u4[3]));
+                        }
                     }
                 }
                 fence_proxy_async();

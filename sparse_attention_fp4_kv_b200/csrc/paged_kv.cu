@@ -1,10 +1,11 @@
 // FP4 append into pages, and the rows back in bf16.
 //
 // The quantization is kv_append.cu's own (kv_quant.cuh), the destination of a
-// row comes from its sequence's page table. One thread per scale group, as in
+// row comes from its sequence's page table. One lane per scale group, as in
 // the contiguous append: a row of 512 channels is one warp, so its loads (32 B
 // per lane), code stores (8 B) and scale stores (1 B) are coalesced, and the
-// 32 lanes' table look-ups fall on one word.
+// 32 lanes' table look-ups fall on one word. Bound by memory; what it takes is
+// loads in flight and CTAs that have work.
 #include "kv_quant.cuh"
 #include "paged.cuh"
 
@@ -15,43 +16,65 @@ namespace csa2 {
 namespace pkv {
 
 constexpr int THREADS = 256;
+constexpr int BATCH = 4;  // groups of a thread, all loaded before the first is stored
+constexpr int PER_CTA = THREADS * BATCH;
 
-// Row (b, i) and group g of work item gid; false when the row is to be skipped,
-// else its row in the pool.
-__device__ __forceinline__ bool locate(int64_t gid, int G, int B, int n, const int64_t *start,
-                                       const int32_t *n_valid, const PagedKv &pk, int &g, int64_t &row,
-                                       int64_t &cell) {
-    row = gid / G;
-    g = (int)(gid - row * G);
-    const int64_t b = row / n;
-    const int i = (int)(row - b * n);
-    if (n_valid && i >= __ldg(n_valid + b)) return false;
-    cell = paged_row(pk, b, __ldg(start + b) + i);
-    return cell >= 0;
+// The CTAs of a sequence cover its n rows' groups; those behind n_valid have
+// nothing to do and leave at once, so that a padded batch costs little.
+struct Span {
+    int b, blocks;       // sequence, CTAs per sequence
+    int64_t first, end;  // groups of the sequence: this CTA's first, and behind the last valid row's
+};
+__device__ __forceinline__ Span span_of(int G, int n, const int32_t *n_valid, int blocks) {
+    Span s;
+    s.blocks = blocks;
+    s.b = blockIdx.x / blocks;
+    s.first = (int64_t)(blockIdx.x - s.b * blocks) * PER_CTA;
+    int rows = n;
+    if (n_valid) {
+        const int v = __ldg(n_valid + s.b);
+        rows = v < n ? v : n;
+    }
+    s.end = (int64_t)rows * G;
+    return s;
 }
 
 template <bool MX>
 __global__ void __launch_bounds__(THREADS)
-    append_kernel(const uint16_t *__restrict__ kv, int B, int n, int C, const int64_t *__restrict__ start,
-                  const int32_t *__restrict__ n_valid, PagedKv pk, uint8_t *__restrict__ fp4,
+    append_kernel(const uint16_t *__restrict__ kv, int n, int C, const int64_t *__restrict__ start,
+                  const int32_t *__restrict__ n_valid, PagedKv pk, int blocks, uint8_t *__restrict__ fp4,
                   uint8_t *__restrict__ sf) {
-    constexpr int GC = MX ? 32 : 16;
+    constexpr int GC = MX ? 32 : 16, LOADS = GC / 8;
     const int G = C / GC;
-    const int64_t gid = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    if (gid >= (int64_t)B * n * G) return;
-    int g;
-    int64_t row, cell;
-    if (!locate(gid, G, B, n, start, n_valid, pk, g, row, cell)) return;
-    const uint4 *src = reinterpret_cast<const uint4 *>(kv + row * C + (int64_t)g * GC);
-    uint8_t *dst = fp4 + cell * (C / 2) + (int64_t)g * (GC / 2);
-    uint32_t scode;
-    if constexpr (MX) {
-        const uint4 a[4] = {src[0], src[1], src[2], src[3]};
-        *reinterpret_cast<uint4 *>(dst) = mxfp4_quant32(a, scode);
-    } else {
-        *reinterpret_cast<uint2 *>(dst) = fp4_quant16(src[0], src[1], scode);
+    const Span s = span_of(G, n, n_valid, blocks);
+    if (s.first >= s.end) return;
+    const int64_t pos0 = __ldg(start + s.b);
+    uint4 x[BATCH][LOADS];
+    int64_t cell[BATCH];
+    int g[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) {
+        const int64_t at = s.first + k * THREADS + threadIdx.x;
+        cell[k] = -1;
+        if (at >= s.end) continue;
+        const int64_t i = at / G;
+        g[k] = (int)(at - i * G);
+        const uint4 *src = reinterpret_cast<const uint4 *>(kv + ((int64_t)s.b * n + i) * C + g[k] * GC);
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) x[k][j] = ld_stream_v4(src + j);
+        cell[k] = paged_row(pk, s.b, pos0 + i);
     }
-    sf[cell * G + g] = (uint8_t)scode;
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) {
+        if (cell[k] < 0) continue;
+        uint8_t *dst = fp4 + cell[k] * (C / 2) + g[k] * (GC / 2);
+        uint32_t scode;
+        if constexpr (MX)
+            *reinterpret_cast<uint4 *>(dst) = mxfp4_quant32(x[k], scode);
+        else
+            *reinterpret_cast<uint2 *>(dst) = fp4_quant16(x[k][0], x[k][1], scode);
+        sf[cell[k] * G + g[k]] = (uint8_t)scode;
+    }
 }
 
 // Eight codes -> eight bf16 values times the scale (exact: 2 + 4 significant bits).
@@ -70,26 +93,44 @@ __device__ __forceinline__ uint4 dequant8(uint32_t codes, float s) {
 template <bool MX>
 __global__ void __launch_bounds__(THREADS)
     gather_kernel(const uint8_t *__restrict__ fp4, const uint8_t *__restrict__ sf, PagedKv pk,
-                  const int64_t *__restrict__ start, const int32_t *__restrict__ n_valid, int B, int n,
-                  int C, uint16_t *__restrict__ out) {
+                  const int64_t *__restrict__ start, const int32_t *__restrict__ n_valid, int n, int C, int blocks,
+                  uint16_t *__restrict__ out) {
     const int G = C / 16;  // 16 channels per thread in both formats
-    const int64_t gid = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    if (gid >= (int64_t)B * n * G) return;
-    int g;
-    int64_t row, cell;
-    if (!locate(gid, G, B, n, start, n_valid, pk, g, row, cell)) return;
-    const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(fp4 + cell * (C / 2) + (int64_t)g * 8));
-    const float s = MX ? e8m0_to_f32(__ldg(sf + cell * (C / 32) + (g >> 1)))
-                       : e4m3_to_f32(__ldg(sf + cell * G + g));
-    uint4 *dst = reinterpret_cast<uint4 *>(out + row * C + (int64_t)g * 16);
-    dst[0] = dequant8(codes.x, s);
-    dst[1] = dequant8(codes.y, s);
+    const Span s = span_of(G, n, n_valid, blocks);
+    if (s.first >= s.end) return;
+    const int64_t pos0 = __ldg(start + s.b);
+    uint2 codes[BATCH];
+    uint32_t scale[BATCH];
+    int64_t to[BATCH];  // group of out, < 0: none
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) {
+        const int64_t at = s.first + k * THREADS + threadIdx.x;
+        to[k] = -1;
+        if (at >= s.end) continue;
+        const int64_t i = at / G;
+        const int g = (int)(at - i * G);
+        const int64_t cell = paged_row(pk, s.b, pos0 + i);
+        if (cell < 0) continue;
+        to[k] = ((int64_t)s.b * n + i) * G + g;
+        codes[k] = __ldg(reinterpret_cast<const uint2 *>(fp4 + cell * (C / 2) + g * 8));
+        scale[k] = MX ? __ldg(sf + cell * (C / 32) + (g >> 1)) : __ldg(sf + cell * G + g);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) {
+        if (to[k] < 0) continue;
+        const float v = MX ? e8m0_to_f32(scale[k]) : e4m3_to_f32(scale[k]);
+        uint4 *dst = reinterpret_cast<uint4 *>(out + to[k] * 16);
+        dst[0] = dequant8(codes[k].x, v);
+        dst[1] = dequant8(codes[k].y, v);
+    }
 }
 
-int grid_of(int64_t items, dim3 &grid) {
-    const int64_t blocks = (items + THREADS - 1) / THREADS;
-    if (blocks > INT32_MAX) return CSA2_ERR_SHAPE;
-    grid = dim3((unsigned)blocks);
+// CTAs per sequence, and the grid.
+int grid_of(int B, int64_t groups, int &blocks, dim3 &grid) {
+    const int64_t per = (groups + PER_CTA - 1) / PER_CTA;
+    if (per * B > INT32_MAX) return CSA2_ERR_SHAPE;
+    blocks = (int)per;
+    grid = dim3((unsigned)(per * B));
     return CSA2_OK;
 }
 
@@ -104,11 +145,12 @@ int append(const void *kv, int B, int n, int C, const int64_t *start, const int3
     if (!aligned(kv, 16) || !aligned(fp4, MX ? 16 : 8)) return CSA2_ERR_ALIGN;
     if ((int64_t)B * n == 0) return CSA2_OK;
     dim3 grid;
-    const int st = grid_of((int64_t)B * n * (C / GC), grid);
+    int blocks;
+    const int st = grid_of(B, (int64_t)n * (C / GC), blocks, grid);
     if (st != CSA2_OK) return st;
     return launch_kernel(false, append_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream,
-                         (const uint16_t *)kv, B, n, C, start, n_valid,
-                         PagedKv{table, max_pages, page_size, n_pages}, fp4, sf);
+                         (const uint16_t *)kv, n, C, start, n_valid,
+                         PagedKv{table, max_pages, page_size, n_pages}, blocks, fp4, sf);
 }
 
 template <bool MX>
@@ -122,10 +164,11 @@ int gather(const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_
     if (!aligned(out, 16) || !aligned(fp4, 8)) return CSA2_ERR_ALIGN;
     if ((int64_t)B * n == 0) return CSA2_OK;
     dim3 grid;
-    const int st = grid_of((int64_t)B * n * (C / 16), grid);
+    int blocks;
+    const int st = grid_of(B, (int64_t)n * (C / 16), blocks, grid);
     if (st != CSA2_OK) return st;
     return launch_kernel(false, gather_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream, fp4, sf,
-                         PagedKv{table, max_pages, page_size, n_pages}, start, n_valid, B, n, C,
+                         PagedKv{table, max_pages, page_size, n_pages}, start, n_valid, n, C, blocks,
                          (uint16_t *)out);
 }
 

@@ -32,9 +32,8 @@ struct Args {
     int64_t xt, xh, ot, oh; // strides in elements
     int tt, hh;             // tile: tokens x heads
     int htiles;             // ceil(H / hh)
-    int per_row;            // work items per row
-    int nrot;               // the first nrot items of a row are rotated, the rest copied
-    uint32_t m_row, m_hh;   // magic numbers for / per_row and / hh
+    int nrot, ncopy;        // rotated and copied items of a row
+    uint32_t m_rot, m_copy, m_hh;  // magic numbers for / nrot, / ncopy and / hh
 };
 
 // n / d for n, d < 2^16 with m = ceil(2^32 / d) (m = 0: d = 1)
@@ -93,58 +92,72 @@ __device__ __forceinline__ void fill_table(const Args &a, int64_t t0, float2 *ta
     }
 }
 
-// Items of a row, 16 bytes (N channels) each: the rotated ones first. In the
-// half layout a rotated item is two pieces, N channels of either half.
+// Items of a row, 16 bytes (N channels) each: the copied pieces first, then the
+// rotated ones. In the half layout a rotated item is two pieces, N channels of
+// either half; they have a loop of their own, because their registers in the copies'
+// loop cost occupancy (36 us for 69,632 rows of 512 channels with 64 rotated, at 75
+// registers; the floor is 22).
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(THREADS) vec_kernel(const Args a) {
     constexpr int N = 16 / sizeof(E);
     extern __shared__ float2 table[];
     const int64_t t0 = (int64_t)(blockIdx.x / a.htiles) * a.tt;
     const int h0 = (int)(blockIdx.x % a.htiles) * a.hh;
-    const int items = a.tt * a.hh * a.per_row;
+    const int rows = a.tt * a.hh;
     const E *x = static_cast<const E *>(a.x);
     E *out = static_cast<E *>(a.out);
+    bool filled = false;
 
-    for (int base = 0; base < items; base += THREADS * BATCH) {
-        uint4 w[BATCH], w2[HALF ? BATCH : 1];
-        int64_t off_out[BATCH];  // < 0: no item
-        int entry[BATCH];        // table entry of the first pair, < 0: copied
+    const int copies = rows * a.ncopy;
+    for (int base = 0; base < copies; base += THREADS * BATCH) {
+        uint4 w[BATCH];
+        int64_t to[BATCH];  // < 0: no item
 #pragma unroll
         for (int k = 0; k < BATCH; k++) {
             const int i = base + k * THREADS + (int)threadIdx.x;
-            const int row = (int)fast_div((uint32_t)i, a.m_row);
-            const int piece = i - row * a.per_row;
-            const int t = (int)fast_div((uint32_t)row, a.m_hh);
-            const int h = h0 + row - t * a.hh;
-            const bool in = i < items && t0 + t < a.T && h < a.H;
-            const bool turn = piece < a.nrot;
-            int c;  // first channel of the item
-            if (turn) {
-                c = a.start + piece * N;
-            } else {
-                c = (piece - a.nrot) * N;
-                if (c >= a.start) c += a.rot;
-            }
-            off_out[k] = in ? (t0 + t) * a.ot + (int64_t)h * a.oh + c : -1;
-            entry[k] = turn ? t * (a.rot / 2) + (HALF ? piece * N : piece * (N / 2)) : -1;
+            const int row = (int)fast_div((uint32_t)i, a.m_copy);
+            const int t = (int)fast_div((uint32_t)row, a.m_hh), h = h0 + row - t * a.hh;
+            int c = (i - row * a.ncopy) * N;
+            if (c >= a.start) c += a.rot;
+            const bool in = i < copies && t0 + t < a.T && h < a.H;
+            to[k] = in ? (t0 + t) * a.ot + (int64_t)h * a.oh + c : -1;
+            if (in) w[k] = ld_stream_v4(x + (t0 + t) * a.xt + (int64_t)h * a.xh + c);
+        }
+        if (!filled) {  // while the first loads are in flight
+            fill_table(a, t0, table);
+            filled = true;
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; k++)
+            if (to[k] >= 0) *reinterpret_cast<uint4 *>(out + to[k]) = w[k];
+    }
+    if (!filled) fill_table(a, t0, table);
+    __syncthreads();
+
+    constexpr int RB = HALF ? 2 : BATCH;
+    const int turns = rows * a.nrot;
+    for (int base = 0; base < turns; base += THREADS * RB) {
+        uint4 w[RB], w2[HALF ? RB : 1];
+        int64_t to[RB];
+        int entry[RB];  // table entry of the first pair
+#pragma unroll
+        for (int k = 0; k < RB; k++) {
+            const int i = base + k * THREADS + (int)threadIdx.x;
+            const int row = (int)fast_div((uint32_t)i, a.m_rot);
+            const int t = (int)fast_div((uint32_t)row, a.m_hh), h = h0 + row - t * a.hh;
+            const int piece = i - row * a.nrot, c = a.start + piece * N;
+            const bool in = i < turns && t0 + t < a.T && h < a.H;
+            to[k] = in ? (t0 + t) * a.ot + (int64_t)h * a.oh + c : -1;
+            entry[k] = t * (a.rot / 2) + (HALF ? piece * N : piece * (N / 2));
             if (in) {
                 const E *src = x + (t0 + t) * a.xt + (int64_t)h * a.xh + c;
                 w[k] = *reinterpret_cast<const uint4 *>(src);
-                if (HALF && turn) w2[HALF ? k : 0] = *reinterpret_cast<const uint4 *>(src + a.rot / 2);
+                if constexpr (HALF) w2[k] = *reinterpret_cast<const uint4 *>(src + a.rot / 2);
             }
-        }
-        if (base == 0) {  // while the first loads are in flight
-            fill_table(a, t0, table);
-            __syncthreads();
         }
 #pragma unroll
-        for (int k = 0; k < BATCH; k++) {
-            if (off_out[k] < 0) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>(out + off_out[k]);
-            if (entry[k] < 0) {
-                *dst = w[k];
-                continue;
-            }
+        for (int k = 0; k < RB; k++) {
+            if (to[k] < 0) continue;
             const float2 *cs = table + entry[k];
             float u[N];
             unpack<E>(w[k], u);
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(THREADS) vec_kernel(const Args a) {
                     u[j] = r.x;
                     v[j] = r.y;
                 }
-                *reinterpret_cast<uint4 *>(out + off_out[k] + a.rot / 2) = pack<E>(v);
+                *reinterpret_cast<uint4 *>(out + to[k] + a.rot / 2) = pack<E>(v);
             } else {
 #pragma unroll
                 for (int j = 0; j < N; j += 2) {
@@ -166,7 +179,7 @@ __global__ void __launch_bounds__(THREADS) vec_kernel(const Args a) {
                     u[j + 1] = r.y;
                 }
             }
-            *dst = pack<E>(u);
+            *reinterpret_cast<uint4 *>(out + to[k]) = pack<E>(u);
         }
     }
 }
@@ -177,11 +190,11 @@ __global__ void __launch_bounds__(THREADS) scalar_kernel(const Args a) {
     extern __shared__ float2 table[];
     const int64_t t0 = (int64_t)(blockIdx.x / a.htiles) * a.tt;
     const int h0 = (int)(blockIdx.x % a.htiles) * a.hh;
-    const int items = a.tt * a.hh * a.per_row;
+    const int per_row = a.nrot + a.ncopy, items = a.tt * a.hh * per_row;
     fill_table(a, t0, table);
     __syncthreads();
     for (int i = threadIdx.x; i < items; i += THREADS) {
-        const int row = i / a.per_row, piece = i - row * a.per_row;
+        const int row = i / per_row, piece = i - row * per_row;
         const int t = row / a.hh, h = h0 + row - t * a.hh;
         if (t0 + t >= a.T || h >= a.H) continue;
         const E *x = static_cast<const E *>(a.x) + (t0 + t) * a.xt + (int64_t)h * a.xh;
@@ -222,9 +235,13 @@ int launch(Args a, bool half, cudaStream_t s) {
                      (half ? a.rot / 2 : a.rot) % N == 0 && a.D % N == 0;
     const int rest = in_place ? 0 : a.D - a.rot;
     a.nrot = vec ? (half ? a.rot / 2 / N : a.rot / N) : a.rot / 2;
-    a.per_row = a.nrot + (vec ? rest / N : rest);
+    a.ncopy = vec ? rest / N : rest;
     // rows of a tile: two batches of 16-byte accesses per thread
-    const int want = 2 * BATCH * THREADS / a.per_row;
+    int want = 2 * BATCH * THREADS / (a.nrot + a.ncopy);
+    // fewer where a small call would leave SMs idle (4 tokens x 64 heads: 5.2 us with 8
+    // CTAs, 3.8 with 16)
+    const int64_t spread = a.T * a.H / (2 * num_sms());
+    if (spread < want) want = (int)spread;
     const int rows = want < 1 ? 1 : want;
     if (rows >= a.H) {
         a.hh = a.H;
@@ -237,7 +254,8 @@ int launch(Args a, bool half, cudaStream_t s) {
         a.tt = 1;
     }
     a.htiles = (a.H + a.hh - 1) / a.hh;
-    a.m_row = magic(a.per_row);
+    a.m_rot = magic(a.nrot);
+    a.m_copy = a.ncopy ? magic(a.ncopy) : 0;
     a.m_hh = magic(a.hh);
     const int64_t blocks = ((a.T + a.tt - 1) / a.tt) * a.htiles;
     if (blocks > INT32_MAX) return CSA2_ERR_SHAPE;

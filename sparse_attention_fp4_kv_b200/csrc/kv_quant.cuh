@@ -6,9 +6,21 @@
 
 namespace csa2 {
 
+// A value with the E2M1 code of the IEEE quotient x / s, for bf16 x, an E4M3 s and
+// inv = 1 / s (fp32). The code asks on which side of a tie t (0.25 .75 1.25 1.75 2.5
+// 3.5 5) the quotient lies, or whether it is one. x has 8 significant bits, s 4 and t
+// 3, so a quotient that is not t is off it by 1 part in 255 at least; x * inv is
+// off by 2^-23. Rounded to 16 significant bits it is t where the quotient is, and
+// on the quotient's side where it is not: a product, two clamps (which make NaN 8,
+// as the conversion does) and two integer steps, a third of a division's cost.
+__device__ __forceinline__ float quotient_for_e2m1(float x, float inv) {
+    const float q = fmaxf(fminf(x * inv, 8.0f), -8.0f);
+    return __uint_as_float((__float_as_uint(q) + 0x80u) & ~0xFFu);
+}
+
 // 16 channels (two 16-byte loads of bf16) -> eight packed code bytes and the
-// E4M3 scale code: s = E4M3(amax / 6), code = E2M1(x / s), +0 where s is 0.
-// Both divisions are IEEE fp32.
+// E4M3 scale code: s = E4M3(amax / 6) by IEEE division, code = E2M1(x / s), +0
+// where s is 0.
 __device__ __forceinline__ uint2 fp4_quant16(uint4 a, uint4 c, uint32_t &scode) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
     float x[16];
@@ -25,9 +37,10 @@ __device__ __forceinline__ uint2 fp4_quant16(uint4 a, uint4 c, uint32_t &scode) 
     const float s = e4m3_to_f32(scode);
     uint32_t lo = 0, hi = 0;
     if (s != 0.0f) {
+        const float inv = __fdiv_rn(1.0f, s);
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; j++) v[j] = __fdiv_rn(x[j], s);
+        for (int j = 0; j < 16; j++) v[j] = quotient_for_e2m1(x[j], inv);
         lo = f32x8_to_e2m1x8(v);
         hi = f32x8_to_e2m1x8(v + 8);
     }

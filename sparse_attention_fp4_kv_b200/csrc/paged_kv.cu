@@ -6,17 +6,15 @@
 // per lane), code stores (8 B) and scale stores (1 B) are coalesced, and the
 // 32 lanes' table look-ups fall on one word. Bound by memory; what it takes is
 // loads in flight and CTAs that have work.
+#include "fp4_rows.cuh"
 #include "kv_quant.cuh"
 #include "paged.cuh"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace csa2 {
 namespace pkv {
 
-constexpr int THREADS = 256;
-constexpr int BATCH = 4;  // groups of a thread, all loaded before the first is stored
+constexpr int THREADS = 128;
+constexpr int BATCH = 2;  // groups of a thread, all loaded before the first is stored
 constexpr int PER_CTA = THREADS * BATCH;
 
 // The CTAs of a sequence cover its n rows' groups; those behind n_valid have
@@ -77,19 +75,6 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-// Eight codes -> eight bf16 values times the scale (exact: 2 + 4 significant bits).
-__device__ __forceinline__ uint4 dequant8(uint32_t codes, float s) {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const uint32_t byte = codes >> (8 * j);
-        const __nv_bfloat162 h =
-            __floats2bfloat162_rn(e2m1_to_f32(byte & 15) * s, e2m1_to_f32((byte >> 4) & 15) * s);
-        o[j] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 template <bool MX>
 __global__ void __launch_bounds__(THREADS)
     gather_kernel(const uint8_t *__restrict__ fp4, const uint8_t *__restrict__ sf, PagedKv pk,
@@ -118,10 +103,10 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int k = 0; k < BATCH; k++) {
         if (to[k] < 0) continue;
-        const float v = MX ? e8m0_to_f32(scale[k]) : e4m3_to_f32(scale[k]);
+        const MxScale s2 = MX ? mx_scale(scale[k]) : e4m3_scale(scale[k]);
         uint4 *dst = reinterpret_cast<uint4 *>(out + to[k] * 16);
-        dst[0] = dequant8(codes[k].x, v);
-        dst[1] = dequant8(codes[k].y, v);
+        dst[0] = rows_bf16(codes[k].x, s2);
+        dst[1] = rows_bf16(codes[k].y, s2);
     }
 }
 

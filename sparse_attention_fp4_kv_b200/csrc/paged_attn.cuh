@@ -138,7 +138,7 @@ __device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (i
 template <bool MX, int U, int NH>
 struct Layout {
     static constexpr int PARTS = MX ? 2 : 1;       // of the weights
-    static constexpr int NP = MX && U == 4 && NH == 64 ? 1 : 2;  // buffers of weights
+    static constexpr int NP = U == 4 && NH == 64 ? 1 : 2;  // buffers of weights (8 x 128K: 221 us with one, 233 with two)
     static constexpr int P_PART = TK * NH * 2;
     static constexpr int Q_CHUNK = NH * 128;       // 64 channels of Q
     static constexpr int Q_OFF = 0;
@@ -180,7 +180,8 @@ static __device__ __forceinline__ void raise_abort(volatile int *abort) {
     atomicExch(&g_paged_attn_error, 1);
 }
 // Wait for a phase, suspended in try_wait; false at once when the CTA has
-// aborted, or, raising the abort, when WAIT_NS pass.
+// aborted, or, raising the abort, when WAIT_NS pass. Lanes may then differ: what
+// holds warp-wide operations goes by all_ok of the lanes' answers.
 static __device__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
     if (test_wait(bar, parity)) return true;
     uint64_t t0 = 0;
@@ -198,6 +199,7 @@ static __device__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abo
         }
     }
 }
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
 
 // ---------------------------------------------------------------- tensor memory
 // N columns (8, 16 or 32) of a warp's 32 lanes, thread t its lane t.
@@ -532,16 +534,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
                     x[i + 3] = fmaf(x[i + 3], f.w, r.w);
                 }
             };
-            // ---- does a score exceed its head's reference by 2^8?
+            // ---- does a score exceed its head's reference by 2^8? The vote also tells of a
+            // wait that ran out; the group then leaves the loop together, so that its
+            // barriers never part.
             bool move = first;
             if (!first) {
                 exponents();
                 float over = x[0];
 #pragma unroll
                 for (int i = 1; i < NC; i++) over = fmaxf(over, x[i]);
-                move = named_bar_or(bar_id, 128, see && over > RESCALE_LOG2 + P_OFFSET);
+                move = named_bar_or(bar_id, 128, !ok || (see && over > RESCALE_LOG2 + P_OFFSET));
             }
             if (move) {
+                if (named_bar_or(bar_id, 128, !ok)) break;
                 // rare: the scores are read again
                 float y[NC];
                 tmem_load_half<NC>(tmem + lanes + ((16u * sr.i) << 16) + U * NH + part * NG, y);
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         uint4 code[L::NS][2];
         uint32_t scl[L::NS][2];  // one E8M0 byte, or two E4M3; as loaded
         auto load_tile = [&]() {
-            ok = wait_bar(bar(L::B_RFULL + rr.i), rr.phase, abort) && ok;
+            ok = all_ok(wait_bar(bar(L::B_RFULL + rr.i), rr.phase, abort) && ok);
             const volatile int64_t *rows = reinterpret_cast<const volatile int64_t *>(sm + L::ROW_OFF) + rr.i * TK + r;
             const int64_t row[2] = {rows[0], rows[4]};
             __syncwarp();
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         for (int k = 0; k < n_tiles; k++) {
             const TileInfo info = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING);
             const int keys = (info.flags >> 8) * 16;
-            if (info.flags & kFirst) {
+            if (ok && (info.flags & kFirst)) {
                 // ---- queries of a new pair: one warp a head, lanes over channels
                 ok = wait_bar(bar(L::B_QFREE), (seg & 1) ^ 1, abort) && ok;
                 float *qf = reinterpret_cast<float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH;
@@ -839,7 +844,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             }
         };
         look_up();
-        for (int k = 0; k < n_tiles && ok; k++) {
+        for (int k = 0; k < n_tiles && all_ok(ok); k++) {
             int64_t row[2];
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         uint32_t seg = 0;
         Ring<2> sr;
         Ring<L::NT> ur;
-        for (int k = 0; k < n_tiles && ok; k++) {
+        for (int k = 0; k < n_tiles && all_ok(ok); k++) {
             if (first) ok = wait_bar(bar(L::B_QFULL), seg & 1, abort) && ok;
             ok = wait_bar(bar(L::B_SFREE + sr.i), sr.phase ^ 1, abort) && ok;
             const uint32_t sd = tmem + ((16u * sr.i) << 16) + U * NH;
@@ -931,7 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         uint32_t seg = 0;
         Ring<L::NP> pr;
         Ring<L::NT> ur;
-        for (int k = 0; k < n_tiles && ok; k++) {
+        for (int k = 0; k < n_tiles && all_ok(ok); k++) {
             // the softmax warps' barrier carries the load warps' info on to here
             ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS), ur.phase, abort) && ok;
             const int flags = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING).flags, steps = flags >> 8;

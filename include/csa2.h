@@ -595,7 +595,8 @@ int csa2_pages_compact(const int32_t *page_table, int S, int max_pages, const in
  *  ctx_len [B] int64 (device); above max_pages * page_size it counts as that
  *  kv_fp4  16-byte aligned, kv_sf 4-byte aligned (MXFP4: any)
  *  C % 32 == 0, 32 <= C <= 512; 1 <= Hq <= 256; n_win >= 0, n_sink >= 0;
- *  max_pages * page_size < 2^31
+ *  max_pages * page_size < 2^31, and
+ *  B * ceil(Hq / 64) * (max_pages * page_size / 64 + 1) < 2^31
  *  ws/ws_bytes: at least csa2_paged_attn_workspace_size(...) bytes, 16-byte
  *  aligned; it starts with the call's error word (csa2_workspace_status), the
  *  rest need not be cleared. Calls that may overlap, graphs among them, need

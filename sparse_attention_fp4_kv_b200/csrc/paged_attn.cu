@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int
     const int chunk = item % chunks, hh = item / chunks % NH, pair = item / chunks / NH;
     const int b = pair / a.groups, g = pair % a.groups, h = g * NH + hh, c = 128 * chunk + 4 * lane;
     if (h >= a.Hq) return;
-    const int64_t T = a.prefix[a.B] * a.groups, p0 = a.prefix[b], tiles = a.prefix[b + 1] - p0;
+    const int p0 = a.prefix[b], tiles = a.prefix[b + 1] - p0;
     uint2 *out = reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.Hq + h) * a.C + c);
     float *lse = a.lse && chunk == 0 && lane == 0 ? a.lse + (int64_t)b * a.Hq + h : nullptr;
     if (tiles == 0) {
@@ -46,13 +46,12 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int
         if ((!WIDE || warp == 0) && lse) *lse = -INFINITY;
         return;
     }
-    const int64_t t0 = p0 * a.groups + g * tiles;
-    const int sharers = sharing(T, G);
-    const int lo = owner_of(t0, T, sharers), hi = owner_of(t0 + tiles - 1, T, sharers);
+    const Shares shares(a.prefix[a.B] * a.groups, G);
+    const int t0 = p0 * a.groups + g * tiles, lo = shares.owner(t0), hi = shares.owner(t0 + tiles - 1);
     if (lo == hi) return;
     const int n = hi - lo + 1;
     // the part of the first CTA: its second segment unless its share starts here
-    const int slot0 = 2 * lo + (share_begin(lo, T, sharers) != t0 ? 1 : 0);
+    const int slot0 = 2 * lo + (shares.begin(lo) != t0 ? 1 : 0);
     auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (lo + i); };
     float m = REF_NONE, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -118,7 +117,7 @@ constexpr size_t up(size_t x) { return (x + 255) / 256 * 256; }
 // and two parts per CTA.
 struct Ws {
     int *err, *flags;
-    int64_t *prefix;
+    int *prefix;
     float *ml, *o;
     size_t bytes;
 };
@@ -134,7 +133,7 @@ Ws layout(void *base, int B, int Hq, int C, int G) {
     };
     w.err = reinterpret_cast<int *>(take(sizeof(int)));
     w.flags = reinterpret_cast<int *>(take(sizeof(int) * (size_t)G));
-    w.prefix = reinterpret_cast<int64_t *>(take(sizeof(int64_t) * ((size_t)B + 1)));
+    w.prefix = reinterpret_cast<int *>(take(sizeof(int) * ((size_t)B + 1)));
     w.ml = reinterpret_cast<float *>(take(sizeof(float) * 2 * 2 * (size_t)G * nh));
     w.o = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)G * nh * pitch));
     w.bytes = off;
@@ -162,7 +161,8 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
     const int G = grid_ctas(), nh = group_heads(Hq), groups = (Hq + nh - 1) / nh;
     const int pitch = (C + 127) / 128 * 128, chunks = pitch / 128;
     const int64_t work = (int64_t)B * groups * nh * chunks;
-    if (work > INT32_MAX) return CSA2_ERR_SHAPE;
+    // the kernels count tiles in 32 bits
+    if (work > INT32_MAX || (int64_t)B * groups * (cap / TK + 1) > INT32_MAX) return CSA2_ERR_SHAPE;
     const Ws w = layout(ws, B, Hq, C, G);
     if (!ws || ws_bytes < w.bytes) return CSA2_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return CSA2_ERR_ALIGN;

@@ -31,7 +31,8 @@
 // Measured steps: one thread polling two barriers 585 us (128-key tiles, one in
 // the ring), rows read whole lines at a time and a warp that stays together 280, two
 // issuing warps and bulk copies 268, the scout, which takes the walk and the
-// table out of the load warps, 238, loads past L1 229. 128-key tiles
+// table out of the load warps, 238, loads past L1 229, one buffer of weights 223, a
+// prologue of one 32-bit scan 220. 128-key tiles
 // (M = 128 for S) leave room for one tile: 292. 16 load warps, at 72
 // registers, spill: 342.
 //
@@ -90,7 +91,7 @@ struct Args {
     float *lse;
     // workspace
     int *flags;        // [G] a CTA that gave up a wait
-    int64_t *prefix;   // [B + 1] tiles before sequence b
+    int *prefix;       // [B + 1] tiles before sequence b
     float *part_ml;    // [2 G][NH][2]: reference - P_OFFSET, sum
     float *part_o;     // [2 G][NH][128 U]
 };
@@ -130,10 +131,19 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b) {
 }
 
 // T tiles are shared by min(G, T) CTAs, so that none between two that have tiles
-// has none. First tile of CTA c's share, and the CTA of tile t.
-__device__ __forceinline__ int sharing(int64_t T, int G) { return T < G ? (int)T : G; }
-__device__ __forceinline__ int64_t share_begin(int c, int64_t T, int G) { return c * T / G; }
-__device__ __forceinline__ int owner_of(int64_t t, int64_t T, int G) { return (int)(((t + 1) * G - 1) / T); }
+// has none. Share c starts at c T / ctas: the larger shares lie apart (with all of
+// them first, a batch that begins with short sequences took 5 % longer).
+struct Shares {
+    int T, ctas, each, more;
+    __device__ __forceinline__ Shares(int T, int G) : T(T) {
+        ctas = T < G ? T : G;
+        each = ctas ? T / ctas : 0;
+        more = T - each * ctas;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * each + c * more / ctas; }
+    // the share with tile t: the last that starts at or before it
+    __device__ __forceinline__ int owner(int t) const { return (int)((((int64_t)t + 1) * ctas - 1) / T); }
+};
 
 template <bool MX, int U, int NH>
 struct Layout {
@@ -161,7 +171,7 @@ struct Layout {
                          B_SFULL = B_UFREE + MAX_RING, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
                          B_PFREE = B_PFULL + 2, B_OFULL = B_PFREE + 2, B_OFREE = B_OFULL + 1,
                          B_RFULL = B_OFREE + 1, B_RFREE = B_RFULL + ROW_RING, NBARS = B_RFREE + ROW_RING;
-    static constexpr int START_OFF = BAR_OFF + NBARS * 8; // int64 first offset, count; int pair
+    static constexpr int START_OFF = BAR_OFF + NBARS * 8; // int [3]: where the share starts
     static constexpr int TADDR_OFF = START_OFF + 24;
     static constexpr int ABORT_OFF = TADDR_OFF + 4;
     static constexpr int BYTES = ABORT_OFF + 4;
@@ -427,61 +437,67 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     }
     if (warp == S_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
 
-    // ---- this CTA's share of the tiles: totals, then where its first tile lies
-    int64_t *red = reinterpret_cast<int64_t *>(sm + L::RED_OFF);  // [17], and the total at [31]
-    int64_t *start = reinterpret_cast<int64_t *>(sm + L::START_OFF);
-    int64_t total = 0;
-    for (int b = tid; b < a.B; b += THREADS) total += seq_of(a, b).tiles;
+    // ---- this CTA's share of the tiles: the prefix of the sequences' tiles, chunk by
+    // chunk of THREADS of them; one chunk, and one pass, for any usual batch
+    int *red = reinterpret_cast<int *>(sm + L::RED_OFF);
+    int *start = reinterpret_cast<int *>(sm + L::START_OFF);  // tile of the pair, b, g
+    constexpr int WARPS = THREADS / 32;
+    static_assert(WARPS <= 32, "a warp scans the warps' sums");
+    // tiles before this thread's sequence of a chunk; `sum` receives the chunk's
+    auto scan = [&](int v, int &sum) {
+        int x = v;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    if (lane == 0) red[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < THREADS / 32; w++) total += red[w];
-    const int64_t T = total * a.groups;
-    const int sharers = sharing(T, G);
-    const int64_t t_begin = cta < sharers ? share_begin(cta, T, sharers) : T;
-    const int64_t t_end = cta < sharers ? share_begin(cta + 1, T, sharers) : T;
-    {
-        int64_t before = 0;  // tiles of the sequences before this chunk
-        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-            // CTA 0 writes every prefix, the others stop at their first tile
-            if (cta != 0 && (t_begin == t_end || before * a.groups > t_begin)) break;
-            const int b = b0 + tid;
-            const int64_t v = b < a.B ? seq_of(a, b).tiles : 0;
-            int64_t x = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            __syncthreads();
-            if (lane == 31) red[warp] = x;
-            __syncthreads();
-            int64_t at = before + x - v;
-            for (int w = 0; w < THREADS / 32; w++) {
-                if (w < warp) at += red[w];
-                before += red[w];
-            }
-            if (cta == 0 && b < a.B) a.prefix[b] = at;
-            if (t_begin < t_end && at * a.groups <= t_begin && t_begin < (at + v) * a.groups) {
-                start[0] = (t_begin - at * a.groups) % v;
-                reinterpret_cast<int *>(start + 1)[0] = b;
-                reinterpret_cast<int *>(start + 1)[1] = (int)((t_begin - at * a.groups) / v);
-            }
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
         }
-        if (cta == 0 && tid == 0) a.prefix[a.B] = total;
+        __syncthreads();
+        if (lane == 31) red[warp] = x;
+        __syncthreads();
+        int s = lane < WARPS ? red[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        sum = __shfl_sync(0xffffffffu, s, 31);
+        const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+        return (warp > 0 ? before : 0) + x - v;
+    };
+    auto tiles_of = [&](int b) { return b < a.B ? seq_of(a, b).tiles : 0; };
+    int v = tiles_of(tid), sum, at = scan(v, sum), total = sum;
+    for (int b0 = THREADS; b0 < a.B; b0 += THREADS) {
+        int more;
+        scan(tiles_of(b0 + tid), more);
+        total += more;
     }
+    const Shares shares(total * a.groups, G);
+    const int t_begin = cta < shares.ctas ? shares.begin(cta) : 0;
+    const int n_tiles = cta < shares.ctas ? shares.begin(cta + 1) - t_begin : 0;
+    for (int b0 = 0, before = 0; b0 < a.B; b0 += THREADS) {
+        if (b0 > 0) {
+            before += sum;
+            v = tiles_of(b0 + tid);
+            at = scan(v, sum);
+        }
+        const int b = b0 + tid, first = (before + at) * a.groups;
+        if (cta == 0 && b < a.B) a.prefix[b] = before + at;
+        if (n_tiles > 0 && first <= t_begin && t_begin < first + v * a.groups) {
+            start[2] = (t_begin - first) / v;
+            start[0] = t_begin - first - start[2] * v;
+            start[1] = b;
+        }
+    }
+    if (cta == 0 && tid == 0) a.prefix[a.B] = total;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::TADDR_OFF);
-    const int n_tiles = (int)(t_end - t_begin);
     Walk w{};
     if (n_tiles > 0) {
-        w.b = reinterpret_cast<int *>(start + 1)[0];
-        w.g = reinterpret_cast<int *>(start + 1)[1];
-        w.tile = (int)start[0];
+        w.tile = start[0];
+        w.b = start[1];
+        w.g = start[2];
         w.s = seq_of(a, w.b);
     }
 

@@ -526,7 +526,8 @@ def test_attention_scale_sign_and_zero(B):
         attend(B, q, fp4, sf, table, i64([500]), scale=scale)
 
 
-@pytest.mark.parametrize("Bn,Hq,C,page,ctx", [(1, 64, 512, 64, 70001), (3, 8, 128, 48, 30011), (150, 16, 64, 32, 300), (400, 64, 512, 16, 33)])
+@pytest.mark.parametrize("Bn,Hq,C,page,ctx", [(1, 64, 512, 64, 70001), (3, 8, 128, 48, 30011), (150, 16, 64, 32, 300), (400, 64, 512, 16, 33),
+                                               (1300, 80, 32, 16, 130)])
 def test_attention_split_and_batched(B, Bn, Hq, C, page, ctx):
     """Long sequences cut over many CTAs; more sequences than CTAs."""
     r = np.random.RandomState(Bn)

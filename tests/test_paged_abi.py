@@ -128,7 +128,8 @@ def test_attention_refusals(B, mx):
     for k in ("q", "fp4", "sf", "table", "len", "out"):
         assert call(B, name, good, **{k: None}) == NULL
     for change in (dict(B=-1), dict(H=0), dict(H=257), dict(C=0), dict(C=48), dict(C=544), dict(M=0), dict(page=0), dict(N=0),
-                   dict(page=1 << 30, M=1 << 12), dict(page=1 << 16, M=1 << 15)):
+                   dict(page=1 << 30, M=1 << 12), dict(page=1 << 16, M=1 << 15),
+                   dict(page=1 << 16, M=1 << 14, B=32, H=256)):  # 2^31 tiles of 64 keys in all
         assert call(B, name, good, **change) == SHAPE, change
     assert call(B, name, good, win=-1) == RANGE and call(B, name, good, sink=-1) == RANGE
     assert call(B, name, good, q=ODD8) == ALIGN and call(B, name, good, fp4=ODD8) == ALIGN

@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     }
     if (warp == S_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
 
+    grid_dep_wait();
     // ---- this CTA's share of the tiles: the prefix of the sequences' tiles, chunk by
     // chunk of THREADS of them; one chunk, and one pass, for any usual batch
     int *red = reinterpret_cast<int *>(sm + L::RED_OFF);
@@ -1011,7 +1012,7 @@ int launch_one(const Args &a, int G, cudaStream_t s) {
     using L = Layout<MX, U, NH>;
     static PerDevice smem_set;
     if (!set_smem_limit_once(smem_set, attn_kernel<MX, U, NH>, L::BYTES)) return CSA2_ERR_CUDA;
-    return launch_kernel(false, attn_kernel<MX, U, NH>, dim3((unsigned)G), dim3(THREADS), L::BYTES, s, a);
+    return launch_kernel(true, attn_kernel<MX, U, NH>, dim3((unsigned)G), dim3(THREADS), L::BYTES, s, a);
 }
 
 // The kernel for C channels and head groups of nh.

@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(THREADS)
                   uint8_t *__restrict__ sf) {
     constexpr int GC = MX ? 32 : 16, LOADS = GC / 8;
     const int G = C / GC;
+    grid_dep_wait();
+    grid_dep_launch();
     const Span s = span_of(G, n, n_valid, blocks);
     if (s.first >= s.end) return;
     const int64_t pos0 = __ldg(start + s.b);
@@ -81,6 +83,8 @@ __global__ void __launch_bounds__(THREADS)
                   const int64_t *__restrict__ start, const int32_t *__restrict__ n_valid, int n, int C, int blocks,
                   uint16_t *__restrict__ out) {
     const int G = C / 16;  // 16 channels per thread in both formats
+    grid_dep_wait();
+    grid_dep_launch();
     const Span s = span_of(G, n, n_valid, blocks);
     if (s.first >= s.end) return;
     const int64_t pos0 = __ldg(start + s.b);
@@ -133,7 +137,7 @@ int append(const void *kv, int B, int n, int C, const int64_t *start, const int3
     int blocks;
     const int st = grid_of(B, (int64_t)n * (C / GC), blocks, grid);
     if (st != CSA2_OK) return st;
-    return launch_kernel(false, append_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream,
+    return launch_kernel(true, append_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream,
                          (const uint16_t *)kv, n, C, start, n_valid,
                          PagedKv{table, max_pages, page_size, n_pages}, blocks, fp4, sf);
 }
@@ -152,7 +156,7 @@ int gather(const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_
     int blocks;
     const int st = grid_of(B, (int64_t)n * (C / 16), blocks, grid);
     if (st != CSA2_OK) return st;
-    return launch_kernel(false, gather_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream, fp4, sf,
+    return launch_kernel(true, gather_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream, fp4, sf,
                          PagedKv{table, max_pages, page_size, n_pages}, start, n_valid, n, C, blocks,
                          (uint16_t *)out);
 }

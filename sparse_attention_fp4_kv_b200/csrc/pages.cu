@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(FT)
 __global__ void __launch_bounds__(FT)
     free_kernel(int32_t *table, int S, int max_pages, int32_t *ref, int n_pages, int page_size,
                 const int32_t *__restrict__ seq, const int64_t *__restrict__ keep_len) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int s = seq[blockIdx.x];
     if (s < 0 || s >= S) return;
     const int keep = keep_len ? pages_of(keep_len[blockIdx.x], page_size, max_pages) : 0;
@@ -378,6 +380,8 @@ __device__ __forceinline__ void copy_page_unit(const Bufs &b, int src, int dst, 
 
 __global__ void __launch_bounds__(CT)
     copy_kernel(const int32_t *__restrict__ pairs, int F, int n_pages, const __grid_constant__ Bufs b) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int64_t per = b.unit0[b.n], total = per * F;
     for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
         const int f = (int)(i / per);
@@ -508,12 +512,12 @@ int free_list(const int32_t *ref, int n_pages, const Ws &w, const R &r, int n_re
               cudaStream_t s) {
     const int chunks = chunks_of(n_pages);
     if (chunks > 1) {
-        const int st = launch_kernel(false, count_kernel, dim3((unsigned)chunks), dim3(T), 0, s, ref, n_pages,
+        const int st = launch_kernel(true, count_kernel, dim3((unsigned)chunks), dim3(T), 0, s, ref, n_pages,
                                      w.counts);
         if (st != CSA2_OK) return st;
     }
     const unsigned grid = (unsigned)(chunks + (n_req + T / 32 - 1) / (T / 32));
-    return launch_kernel(chunks > 1, free_list_kernel<R>, dim3(grid), dim3(T), 0, s, ref, n_pages, chunks,
+    return launch_kernel(true, free_list_kernel<R>, dim3(grid), dim3(T), 0, s, ref, n_pages, chunks,
                          (const int32_t *)w.counts, w.head, w.list_a, r, n_req, w.need, n_failed);
 }
 
@@ -568,7 +572,7 @@ extern "C" int csa2_pages_free(int32_t *page_table, int S, int max_pages, int32_
     if (F != 0 && (!page_table || !ref || !seq)) return CSA2_ERR_NULL;
     if (!pages::table_ok(S, max_pages, page_size, n_pages) || F < 0) return CSA2_ERR_SHAPE;
     if (F == 0) return CSA2_OK;
-    return launch_kernel(false, pages::free_kernel, dim3((unsigned)F, pages::row_blocks(max_pages)),
+    return launch_kernel(true, pages::free_kernel, dim3((unsigned)F, pages::row_blocks(max_pages)),
                          dim3(pages::FT), 0, (cudaStream_t)stream, page_table, S, max_pages, ref, n_pages,
                          page_size, seq, keep_len);
 }
@@ -582,7 +586,7 @@ extern "C" int csa2_pages_copy(const int32_t *pairs, int F, const csa2_page_buf 
     if (st != CSA2_OK) return st;
     if (F == 0) return CSA2_OK;
     const int64_t units = b.unit0[n_bufs] * F, most = (int64_t)num_sms() * 8;
-    return launch_kernel(false, pages::copy_kernel, dim3((unsigned)(units < most ? units : most)),
+    return launch_kernel(true, pages::copy_kernel, dim3((unsigned)(units < most ? units : most)),
                          dim3(pages::CT), 0, (cudaStream_t)stream, pairs, F, n_pages, b);
 }
 
@@ -603,11 +607,11 @@ extern "C" int csa2_pages_compact(const int32_t *page_table, int S, int max_page
     cudaStream_t s = (cudaStream_t)stream;
     const int chunks = pages::chunks_of(n_pages);
     if (chunks > 1) {
-        st = launch_kernel(false, pages::count_kernel, dim3((unsigned)chunks), dim3(pages::T), 0, s, ref, n_pages,
+        st = launch_kernel(true, pages::count_kernel, dim3((unsigned)chunks), dim3(pages::T), 0, s, ref, n_pages,
                            w.counts);
         if (st != CSA2_OK) return st;
     }
-    st = launch_kernel(chunks > 1, pages::compact_list_kernel, dim3((unsigned)chunks), dim3(pages::T), 0, s, ref,
+    st = launch_kernel(true, pages::compact_list_kernel, dim3((unsigned)chunks), dim3(pages::T), 0, s, ref,
                        n_pages, chunks, (const int32_t *)w.counts, w.head, w.list_a, w.list_b, w.map, n_live);
     if (st != CSA2_OK) return st;
     const int64_t entries = (int64_t)S * max_pages;

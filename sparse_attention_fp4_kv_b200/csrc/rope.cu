@@ -101,6 +101,8 @@ template <typename E, bool HALF>
 __global__ void __launch_bounds__(THREADS) vec_kernel(const Args a) {
     constexpr int N = 16 / sizeof(E);
     extern __shared__ float2 table[];
+    grid_dep_wait();
+    grid_dep_launch();
     const int64_t t0 = (int64_t)(blockIdx.x / a.htiles) * a.tt;
     const int h0 = (int)(blockIdx.x % a.htiles) * a.hh;
     const int rows = a.tt * a.hh;
@@ -188,6 +190,8 @@ __global__ void __launch_bounds__(THREADS) vec_kernel(const Args a) {
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(THREADS) scalar_kernel(const Args a) {
     extern __shared__ float2 table[];
+    grid_dep_wait();
+    grid_dep_launch();
     const int64_t t0 = (int64_t)(blockIdx.x / a.htiles) * a.tt;
     const int h0 = (int)(blockIdx.x % a.htiles) * a.hh;
     const int per_row = a.nrot + a.ncopy, items = a.tt * a.hh * per_row;
@@ -262,11 +266,11 @@ int launch(Args a, bool half, cudaStream_t s) {
     const size_t smem = sizeof(float2) * (size_t)a.tt * (a.rot / 2);
     const dim3 grid((unsigned)blocks), block(THREADS);
     if (vec) {  // a tile has at most 2 BATCH THREADS + D / N < 2^16 items: fast_div holds
-        if (half) return launch_kernel(false, vec_kernel<E, true>, grid, block, smem, s, a);
-        return launch_kernel(false, vec_kernel<E, false>, grid, block, smem, s, a);
+        if (half) return launch_kernel(true, vec_kernel<E, true>, grid, block, smem, s, a);
+        return launch_kernel(true, vec_kernel<E, false>, grid, block, smem, s, a);
     }
-    if (half) return launch_kernel(false, scalar_kernel<E, true>, grid, block, smem, s, a);
-    return launch_kernel(false, scalar_kernel<E, false>, grid, block, smem, s, a);
+    if (half) return launch_kernel(true, scalar_kernel<E, true>, grid, block, smem, s, a);
+    return launch_kernel(true, scalar_kernel<E, false>, grid, block, smem, s, a);
 }
 
 }  // namespace rope

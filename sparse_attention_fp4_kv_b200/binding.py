@@ -348,45 +348,58 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
 
 
 # These calls are a few microseconds each on the device, so the marshalling counts:
-# raw pointers and stream handles go to ctypes as plain integers.
-def _here(stream, *tensors):
-    """The stream handle of a paged call. It launches on the stream's device, which has
-    to be the current one, and refuses tensors of another."""
-    dev = torch.cuda.current_device()
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"the stream is on {stream.device}, the current device is {dev}")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the call runs on device {dev}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+# one check per tensor, and raw pointers and stream handles go to ctypes as plain
+# integers.
+def _device(t, dtype, name: str) -> int:
+    """The device of a call's first tensor, on which the others have to be too."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _addr(t):
-    if t is None:
-        return None
+def _arg(t, dtype, name: str, dev: int) -> int:
+    """The address of a contiguous tensor of this type on this device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
     if not t.is_contiguous():
-        raise ValueError("tensors passed to libcsa2 must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _scratch(nbytes: int, like, stream):
+def _handle(stream, dev: int) -> int:
+    """The stream handle of a call on `dev`, which has to be the current device."""
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _scratch(nbytes: int, device, stream):
     """Workspace of a call that was given none: allocated on the call's stream,
     so that it is not handed out again before the call's kernels have run."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def csa2_rope_freqs(inv_freq, theta: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
                     orig_ctx: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
                     stream=None) -> None:
     """inv_freq [rot_dim / 2] fp64: the table csa2_rope reads."""
-    _want(inv_freq, torch.float64, "inv_freq")
-    st = _here(stream, inv_freq)
+    dev = _device(inv_freq, torch.float64, "inv_freq")
+    table = _arg(inv_freq, torch.float64, "inv_freq", dev)
     _check("csa2_rope_freqs", lib.csa2_rope_freqs(
         2 * inv_freq.numel(), float(theta), scaling, float(factor), orig_ctx, float(beta_fast),
-        float(beta_slow), _addr(inv_freq), st))
+        float(beta_slow), table, _handle(stream, dev)))
 
 
 def csa2_rope(x, pos, inv_freq, out, rot_start: int = 0, interleaved: bool = True,
@@ -394,31 +407,44 @@ def csa2_rope(x, pos, inv_freq, out, rot_start: int = 0, interleaved: bool = Tru
     """x, out [T][H][D] bf16 or fp32 (out may be x; channels contiguous, any token
     and head strides); pos [T] int64; inv_freq [rot_dim / 2] fp64. Rotates the
     channels [rot_start, rot_start + rot_dim) of every head."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    f32 = x.dtype is torch.float32
+    if not f32 and x.dtype is not torch.bfloat16:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    _want(x, x.dtype, "x")
-    _want(out, x.dtype, "out")
-    _want(pos, torch.int64, "pos")
-    _want(inv_freq, torch.float64, "inv_freq")
+    dev = _device(x, x.dtype, "x")
+    if _device(out, x.dtype, "out") != dev:
+        raise ValueError("x and out must be on one device")
+    at = _arg(pos, torch.int64, "pos", dev)
+    table = _arg(inv_freq, torch.float64, "inv_freq", dev)
     T, H, D = x.shape
     assert out.shape == x.shape and pos.shape == (T,) and inv_freq.dim() == 1
-    if D > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+    (xt, xh, xc), (ot, oh, oc) = x.stride(), out.stride()
+    if D > 1 and (xc != 1 or oc != 1):
         raise ValueError("the channels of x and out must be contiguous")
-    st = _here(stream, x, out, pos, inv_freq)
     _check("csa2_rope", lib.csa2_rope(
-        x.data_ptr(), out.data_ptr(), int(x.dtype == torch.float32), _addr(pos), _addr(inv_freq),
+        x.data_ptr(), out.data_ptr(), int(f32), at, table,
         T, H, D, rot_start, 2 * inv_freq.shape[0], 0 if interleaved else 1, int(inverse),
-        float(mscale), x.stride(0), x.stride(1), out.stride(0), out.stride(1), st))
+        float(mscale), xt, xh, ot, oh, _handle(stream, dev)))
 
 
-def _pool(kv_fp4, kv_sf, C: int, mx: bool):
-    """(page_size, n_pages) of a pool kv_fp4 [n_pages][page_size][C/2] and its scales."""
-    _want(kv_fp4, torch.uint8, "kv_fp4")
-    _want(kv_sf, torch.uint8, "kv_sf")
-    n_pages, page_size = kv_fp4.shape[:2]
-    assert kv_fp4.shape == (n_pages, page_size, C // 2)
-    assert kv_sf.shape == (n_pages, page_size, C // (32 if mx else 16))
-    return page_size, n_pages
+def _pool(kv_fp4, kv_sf, C: int, mx: bool, dev: int):
+    """(codes, scales, page_size, n_pages) of a pool kv_fp4 [n_pages][page_size][C/2]."""
+    n_pages, page_size, half = kv_fp4.shape
+    assert half == C // 2 and kv_sf.shape == (n_pages, page_size, C // (32 if mx else 16))
+    return _arg(kv_fp4, torch.uint8, "kv_fp4", dev), _arg(kv_sf, torch.uint8, "kv_sf", dev), page_size, n_pages
+
+
+def _counts(n_valid, B: int, dev: int):
+    if n_valid is None:
+        return None
+    assert n_valid.shape == (B,)
+    return _arg(n_valid, torch.int32, "n_valid", dev)
+
+
+def _table(page_table, S: int, dev: int):
+    """(address, max_pages) of a page table [S][max_pages]."""
+    rows, max_pages = page_table.shape
+    assert rows == S
+    return _arg(page_table, torch.int32, "page_table", dev), max_pages
 
 
 def csa2_paged_kv_append_fp4(kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid=None, stream=None,
@@ -426,40 +452,34 @@ def csa2_paged_kv_append_fp4(kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_va
     """kv_bf16 [B][n_new][C] bf16; start_pos [B] int64; page_table [B][max_pages]
     int32; kv_fp4 [n_pages][page_size][C/2] and kv_sf [..][C/16] (mx: [..][C/32])
     uint8; n_valid [B] int32 or None."""
-    _want(kv_bf16, torch.bfloat16, "kv_bf16")
-    _want(start_pos, torch.int64, "start_pos")
-    _want(page_table, torch.int32, "page_table")
+    dev = _device(kv_bf16, torch.bfloat16, "kv_bf16")
+    rows = _arg(kv_bf16, torch.bfloat16, "kv_bf16", dev)
+    at = _arg(start_pos, torch.int64, "start_pos", dev)
     B, n, C = kv_bf16.shape
-    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
-    assert page_table.shape[0] == B and start_pos.shape == (B,)
-    if n_valid is not None:
-        _want(n_valid, torch.int32, "n_valid")
-        assert n_valid.shape == (B,)
-    st = _here(stream, kv_bf16, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    table, max_pages = _table(page_table, B, dev)
+    codes, scales, page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx, dev)
+    assert start_pos.shape == (B,)
+    valid = _counts(n_valid, B, dev)
     name = "csa2_paged_kv_append_mxfp4" if mx else "csa2_paged_kv_append_fp4"
     _check(name, getattr(lib, name)(
-        _addr(kv_bf16), B, n, C, _addr(start_pos), _addr(n_valid), _addr(page_table), page_table.shape[1],
-        page_size, n_pages, _addr(kv_fp4), _addr(kv_sf), st))
+        rows, B, n, C, at, valid, table, max_pages, page_size, n_pages, codes, scales, _handle(stream, dev)))
 
 
 def csa2_paged_kv_gather(kv_fp4, kv_sf, page_table, start_pos, out, n_valid=None, stream=None,
                          mx: bool = False) -> None:
     """out [B][n][C] bf16 receives the rows at positions start_pos[b] + i; rows
     with i >= n_valid[b] or no page are left as they were."""
-    _want(out, torch.bfloat16, "out")
-    _want(start_pos, torch.int64, "start_pos")
-    _want(page_table, torch.int32, "page_table")
+    dev = _device(out, torch.bfloat16, "out")
+    rows = _arg(out, torch.bfloat16, "out", dev)
+    at = _arg(start_pos, torch.int64, "start_pos", dev)
     B, n, C = out.shape
-    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
-    assert page_table.shape[0] == B and start_pos.shape == (B,)
-    if n_valid is not None:
-        _want(n_valid, torch.int32, "n_valid")
-        assert n_valid.shape == (B,)
-    st = _here(stream, out, start_pos, page_table, kv_fp4, kv_sf, n_valid)
+    table, max_pages = _table(page_table, B, dev)
+    codes, scales, page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx, dev)
+    assert start_pos.shape == (B,)
+    valid = _counts(n_valid, B, dev)
     name = "csa2_paged_kv_gather_mxfp4" if mx else "csa2_paged_kv_gather_fp4"
     _check(name, getattr(lib, name)(
-        _addr(kv_fp4), _addr(kv_sf), _addr(page_table), page_table.shape[1], page_size, n_pages,
-        _addr(start_pos), _addr(n_valid), B, n, C, _addr(out), st))
+        codes, scales, table, max_pages, page_size, n_pages, at, valid, B, n, C, rows, _handle(stream, dev)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -467,85 +487,83 @@ def pages_workspace_size(n_pages: int, n: int = 0) -> int:
     return lib.csa2_pages_workspace_size(n_pages, n)
 
 
-def _pages_ws(ws, n_pages: int, n: int, ref, stream):
+def _workspace(ws, nbytes: int, dev: int, stream):
+    """(tensor, address, bytes) of a call's workspace; nbytes of it are allocated if it was given none."""
     if ws is None:
-        ws = _scratch(pages_workspace_size(n_pages, n), ref, stream)
-    return ws, ws.numel() * ws.element_size()
+        ws = _scratch(nbytes, dev, stream)
+    return ws, _arg(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size()
 
 
-def _want_pages(page_table, ref):
-    _want(page_table, torch.int32, "page_table")
-    _want(ref, torch.int32, "ref")
-    assert page_table.dim() == 2 and ref.dim() == 1
+def _pages(page_table, ref):
+    """(device, table, S, max_pages, counts, n_pages)"""
+    dev = _device(page_table, torch.int32, "page_table")
+    S, max_pages = page_table.shape
+    n_pages, = ref.shape
+    return (dev, _arg(page_table, torch.int32, "page_table", dev), S, max_pages,
+            _arg(ref, torch.int32, "ref", dev), n_pages)
 
 
 def csa2_pages_extend(page_table, ref, want_len, page_size: int, n_failed, ws=None, stream=None) -> None:
     """page_table [S][max_pages] int32; ref [n_pages] int32; want_len [S] int64;
     n_failed [1] int32."""
-    _want_pages(page_table, ref)
-    _want(want_len, torch.int64, "want_len")
-    _want(n_failed, torch.int32, "n_failed")
-    S, M = page_table.shape
+    dev, table, S, M, counts, n_pages = _pages(page_table, ref)
+    want = _arg(want_len, torch.int64, "want_len", dev)
+    failed = _arg(n_failed, torch.int32, "n_failed", dev)
     assert want_len.shape == (S,)
-    st = _here(stream, page_table, ref, want_len, n_failed, ws)
-    ws, wsb = _pages_ws(ws, ref.shape[0], S, ref, stream)
+    st = _handle(stream, dev)
+    ws, wsp, wsb = _workspace(ws, pages_workspace_size(n_pages, S), dev, stream)
     _check("csa2_pages_extend", lib.csa2_pages_extend(
-        _addr(page_table), S, M, _addr(ref), ref.shape[0], page_size, _addr(want_len), _addr(n_failed),
-        _addr(ws), wsb, st))
+        table, S, M, counts, n_pages, page_size, want, failed, wsp, wsb, st))
 
 
 def csa2_pages_fork(page_table, ref, seq_len, src, dst, page_size: int, pairs, n_failed, ws=None,
                     stream=None) -> None:
     """seq_len [S] int64; src, dst [F] int32; pairs [F][2] int32; n_failed [1] int32."""
-    _want_pages(page_table, ref)
-    _want(seq_len, torch.int64, "seq_len")
-    for t, name in ((src, "src"), (dst, "dst"), (pairs, "pairs"), (n_failed, "n_failed")):
-        _want(t, torch.int32, name)
-    S, M = page_table.shape
-    F = src.shape[0]
+    dev, table, S, M, counts, n_pages = _pages(page_table, ref)
+    lens = _arg(seq_len, torch.int64, "seq_len", dev)
+    of, to = _arg(src, torch.int32, "src", dev), _arg(dst, torch.int32, "dst", dev)
+    copies = _arg(pairs, torch.int32, "pairs", dev)
+    failed = _arg(n_failed, torch.int32, "n_failed", dev)
+    F, = src.shape
     assert seq_len.shape == (S,) and dst.shape == (F,) and pairs.shape == (F, 2)
-    st = _here(stream, page_table, ref, seq_len, src, dst, pairs, n_failed, ws)
-    ws, wsb = _pages_ws(ws, ref.shape[0], F, ref, stream)
+    st = _handle(stream, dev)
+    ws, wsp, wsb = _workspace(ws, pages_workspace_size(n_pages, F), dev, stream)
     _check("csa2_pages_fork", lib.csa2_pages_fork(
-        _addr(page_table), S, M, _addr(ref), ref.shape[0], page_size, _addr(seq_len), _addr(src), _addr(dst), F,
-        _addr(pairs), _addr(n_failed), _addr(ws), wsb, st))
+        table, S, M, counts, n_pages, page_size, lens, of, to, F, copies, failed, wsp, wsb, st))
 
 
 def csa2_pages_free(page_table, ref, seq, page_size: int, keep_len=None, stream=None) -> None:
     """seq [F] int32; keep_len [F] int64 or None (nothing is kept)."""
-    _want_pages(page_table, ref)
-    _want(seq, torch.int32, "seq")
-    F = seq.shape[0]
+    dev, table, S, M, counts, n_pages = _pages(page_table, ref)
+    which = _arg(seq, torch.int32, "seq", dev)
+    F, = seq.shape
+    keep = None
     if keep_len is not None:
-        _want(keep_len, torch.int64, "keep_len")
         assert keep_len.shape == (F,)
-    st = _here(stream, page_table, ref, seq, keep_len)
+        keep = _arg(keep_len, torch.int64, "keep_len", dev)
     _check("csa2_pages_free", lib.csa2_pages_free(
-        _addr(page_table), page_table.shape[0], page_table.shape[1], _addr(ref), ref.shape[0], page_size,
-        _addr(seq), _addr(keep_len), F, st))
+        table, S, M, counts, n_pages, page_size, which, keep, F, _handle(stream, dev)))
 
 
-def _page_bufs(bufs, n_pages: int):
+def _page_bufs(bufs, n_pages: int, dev: int):
     """Tensors [n_pages][...] of one cache -> the C array of their bases and page sizes."""
     arr = (csa2_page_buf * max(1, len(bufs)))()
     for a, t in zip(arr, bufs):
-        if not t.is_cuda:
-            raise ValueError("the cache buffers must be CUDA tensors")
         assert t.shape[0] == n_pages
-        a.base = _addr(t)
+        a.base = _arg(t, t.dtype, "a cache buffer", dev)
         a.page_bytes = t.numel() // n_pages * t.element_size()
     return arr
 
 
 def csa2_pages_copy(pairs, bufs: Sequence[torch.Tensor], stream=None) -> None:
     """pairs [F][2] int32 (from, onto); bufs: tensors [n_pages][...] of any dtype."""
-    _want(pairs, torch.int32, "pairs")
-    F = pairs.shape[0]
-    assert pairs.shape == (F, 2) and len(bufs) >= 1
+    dev = _device(pairs, torch.int32, "pairs")
+    copies = _arg(pairs, torch.int32, "pairs", dev)
+    F, two = pairs.shape
+    assert two == 2 and len(bufs) >= 1
     n_pages = bufs[0].shape[0]
-    st = _here(stream, pairs, *bufs)
     _check("csa2_pages_copy", lib.csa2_pages_copy(
-        _addr(pairs), F, _page_bufs(bufs, n_pages), len(bufs), n_pages, st))
+        copies, F, _page_bufs(bufs, n_pages, dev), len(bufs), n_pages, _handle(stream, dev)))
 
 
 def csa2_pages_compact(page_table, ref, bufs: Sequence[torch.Tensor], page_table_out, ref_out, n_live,
@@ -553,16 +571,16 @@ def csa2_pages_compact(page_table, ref, bufs: Sequence[torch.Tensor], page_table
     """page_table, page_table_out [S][max_pages] int32 and ref, ref_out [n_pages]
     int32 (the outputs may be the inputs); bufs: tensors [n_pages][...]; n_live [1]
     int32."""
-    _want_pages(page_table, ref)
-    _want_pages(page_table_out, ref_out)
-    _want(n_live, torch.int32, "n_live")
-    assert page_table_out.shape == page_table.shape and ref_out.shape == ref.shape
-    st = _here(stream, page_table, ref, page_table_out, ref_out, n_live, ws, *bufs)
-    ws, wsb = _pages_ws(ws, ref.shape[0], 0, ref, stream)
+    dev, table, S, M, counts, n_pages = _pages(page_table, ref)
+    table_out = _arg(page_table_out, torch.int32, "page_table_out", dev)
+    counts_out = _arg(ref_out, torch.int32, "ref_out", dev)
+    live = _arg(n_live, torch.int32, "n_live", dev)
+    assert page_table_out.shape == (S, M) and ref_out.shape == (n_pages,)
+    st = _handle(stream, dev)
+    ws, wsp, wsb = _workspace(ws, pages_workspace_size(n_pages, 0), dev, stream)
     _check("csa2_pages_compact", lib.csa2_pages_compact(
-        _addr(page_table), page_table.shape[0], page_table.shape[1], _addr(ref), ref.shape[0],
-        _page_bufs(bufs, ref.shape[0]), len(bufs), _addr(page_table_out), _addr(ref_out), _addr(n_live),
-        _addr(ws), wsb, st))
+        table, S, M, counts, n_pages, _page_bufs(bufs, n_pages, dev), len(bufs), table_out, counts_out, live,
+        wsp, wsb, st))
 
 
 @functools.lru_cache(maxsize=256)
@@ -580,21 +598,21 @@ def csa2_paged_attn_decode(q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, soft
     """q_bf16, out [B][Hq][C] bf16; kv_fp4 [n_pages][page_size][C/2] and kv_sf uint8;
     page_table [B][max_pages] int32; ctx_len [B] int64; lse [B][Hq] fp32 or None;
     n_win = 0 attends every position, else the last n_win and the first n_sink."""
-    _want(q_bf16, torch.bfloat16, "q_bf16")
-    _want(out, torch.bfloat16, "out")
-    _want(page_table, torch.int32, "page_table")
-    _want(ctx_len, torch.int64, "ctx_len")
-    B, Hq, C = q_bf16.shape
-    page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx)
-    assert out.shape == q_bf16.shape and page_table.shape[0] == B and ctx_len.shape == (B,)
+    dev = _device(q_bf16, torch.bfloat16, "q_bf16")
+    q = _arg(q_bf16, torch.bfloat16, "q_bf16", dev)
+    o = _arg(out, torch.bfloat16, "out", dev)
+    lens = _arg(ctx_len, torch.int64, "ctx_len", dev)
+    B, Hq, C = shape = q_bf16.shape
+    table, max_pages = _table(page_table, B, dev)
+    codes, scales, page_size, n_pages = _pool(kv_fp4, kv_sf, C, mx, dev)
+    assert out.shape == shape and ctx_len.shape == (B,)
+    lse_at = None
     if lse is not None:
-        _want(lse, torch.float32, "lse")
         assert lse.shape == (B, Hq)
-    st = _here(stream, q_bf16, kv_fp4, kv_sf, page_table, ctx_len, out, lse, ws)
-    if ws is None:
-        ws = _scratch(_paged_attn_ws(q_bf16.get_device(), B, Hq, C), q_bf16, stream)
+        lse_at = _arg(lse, torch.float32, "lse", dev)
+    st = _handle(stream, dev)
+    ws, wsp, wsb = _workspace(ws, _paged_attn_ws(dev, B, Hq, C), dev, stream)
     name = "csa2_paged_attn_decode_mxfp4" if mx else "csa2_paged_attn_decode"
     _check(name, getattr(lib, name)(
-        _addr(q_bf16), _addr(kv_fp4), _addr(kv_sf), _addr(page_table), page_table.shape[1], page_size,
-        n_pages, _addr(ctx_len), n_win, n_sink, B, Hq, C, float(softmax_scale), _addr(out), _addr(lse),
-        _addr(ws), ws.numel() * ws.element_size(), st))
+        q, codes, scales, table, max_pages, page_size, n_pages, lens, n_win, n_sink, B, Hq, C,
+        float(softmax_scale), o, lse_at, wsp, wsb, st))

@@ -479,7 +479,7 @@ int csa2_rope_freqs(int rot_dim, double theta, int scaling, double factor, int64
  * (b, i) written at position p = start_pos[b] + i of sequence b, in page
  * page_table[b][p / page_size], slot p % page_size. Bytes and scales are those
  * calls' own. Rows with i >= n_valid[b], p < 0 or no page are skipped. Two rows
- * that fall on the same slot leave one of them, which one is unspecified.
+ * that fall on the same slot leave it unspecified.
  *
  *  kv_bf16  [B][n_new][C] bf16, 16-byte aligned; start_pos [B] int64 (device)
  *  n_valid  [B] int32 (device) or NULL (all n_new)

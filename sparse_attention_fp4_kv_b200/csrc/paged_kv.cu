@@ -16,16 +16,21 @@ namespace pkv {
 constexpr int THREADS = 128;
 constexpr int BATCH = 2;  // groups of a thread, all loaded before the first is stored
 constexpr int PER_CTA = THREADS * BATCH;
+constexpr int MOST = 2 * (2048 / THREADS);  // CTAs per SM of a padded call
 
-// The CTAs of a sequence cover its n rows' groups; those behind n_valid have
-// nothing to do and leave at once, so that a padded batch costs little.
+// A CTA takes PER_CTA groups of its sequence. With n_valid most rows may be
+// padding, and CTAs that only find that out are what a large call spends its time
+// on: beyond two waves of CTAs a padded call walks its groups instead, PER_CTA at
+// a time and `step` apart (8 chunks of up to 8192 rows, 8527 in all: append and
+// read-back 12.4 us, with a CTA for every group 15.2; without padding the walk
+// costs, 65,536 rows 38.0 against 36.4).
 struct Span {
-    int b, blocks;       // sequence, CTAs per sequence
-    int64_t first, end;  // groups of the sequence: this CTA's first, and behind the last valid row's
+    int b;                     // sequence
+    int64_t first, end, step;  // groups of the sequence: this CTA's first, and behind the last valid row's
 };
 __device__ __forceinline__ Span span_of(int G, int n, const int32_t *n_valid, int blocks) {
     Span s;
-    s.blocks = blocks;
+    s.step = (int64_t)blocks * PER_CTA;
     s.b = blockIdx.x / blocks;
     s.first = (int64_t)(blockIdx.x - s.b * blocks) * PER_CTA;
     int rows = n;
@@ -36,8 +41,7 @@ __device__ __forceinline__ Span span_of(int G, int n, const int32_t *n_valid, in
     s.end = (int64_t)rows * G;
     return s;
 }
-
-template <bool MX>
+template <bool MX, bool WALK>
 __global__ void __launch_bounds__(THREADS)
     append_kernel(const uint16_t *__restrict__ kv, int n, int C, const int64_t *__restrict__ start,
                   const int32_t *__restrict__ n_valid, PagedKv pk, int blocks, uint8_t *__restrict__ fp4,
@@ -49,35 +53,38 @@ __global__ void __launch_bounds__(THREADS)
     const Span s = span_of(G, n, n_valid, blocks);
     if (s.first >= s.end) return;
     const int64_t pos0 = __ldg(start + s.b);
-    uint4 x[BATCH][LOADS];
-    int64_t cell[BATCH];
-    int g[BATCH];
+    for (int64_t first = s.first; first < s.end; first += s.step) {
+        uint4 x[BATCH][LOADS];
+        int64_t cell[BATCH];
+        int g[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) {
-        const int64_t at = s.first + k * THREADS + threadIdx.x;
-        cell[k] = -1;
-        if (at >= s.end) continue;
-        const int64_t i = at / G;
-        g[k] = (int)(at - i * G);
-        const uint4 *src = reinterpret_cast<const uint4 *>(kv + ((int64_t)s.b * n + i) * C + g[k] * GC);
+        for (int k = 0; k < BATCH; k++) {
+            const int64_t at = first + k * THREADS + threadIdx.x;
+            cell[k] = -1;
+            if (at >= s.end) continue;
+            const int64_t i = at / G;
+            g[k] = (int)(at - i * G);
+            const uint4 *src = reinterpret_cast<const uint4 *>(kv + ((int64_t)s.b * n + i) * C + g[k] * GC);
 #pragma unroll
-        for (int j = 0; j < LOADS; j++) x[k][j] = ld_stream_v4(src + j);
-        cell[k] = paged_row(pk, s.b, pos0 + i);
-    }
+            for (int j = 0; j < LOADS; j++) x[k][j] = ld_stream_v4(src + j);
+            cell[k] = paged_row(pk, s.b, pos0 + i);
+        }
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) {
-        if (cell[k] < 0) continue;
-        uint8_t *dst = fp4 + cell[k] * (C / 2) + g[k] * (GC / 2);
-        uint32_t scode;
-        if constexpr (MX)
-            *reinterpret_cast<uint4 *>(dst) = mxfp4_quant32(x[k], scode);
-        else
-            *reinterpret_cast<uint2 *>(dst) = fp4_quant16(x[k][0], x[k][1], scode);
-        sf[cell[k] * G + g[k]] = (uint8_t)scode;
+        for (int k = 0; k < BATCH; k++) {
+            if (cell[k] < 0) continue;
+            uint8_t *dst = fp4 + cell[k] * (C / 2) + g[k] * (GC / 2);
+            uint32_t scode;
+            if constexpr (MX)
+                *reinterpret_cast<uint4 *>(dst) = mxfp4_quant32(x[k], scode);
+            else
+                *reinterpret_cast<uint2 *>(dst) = fp4_quant16(x[k][0], x[k][1], scode);
+            sf[cell[k] * G + g[k]] = (uint8_t)scode;
+        }
+        if constexpr (!WALK) break;
     }
 }
 
-template <bool MX>
+template <bool MX, bool WALK>
 __global__ void __launch_bounds__(THREADS)
     gather_kernel(const uint8_t *__restrict__ fp4, const uint8_t *__restrict__ sf, PagedKv pk,
                   const int64_t *__restrict__ start, const int32_t *__restrict__ n_valid, int n, int C, int blocks,
@@ -88,35 +95,41 @@ __global__ void __launch_bounds__(THREADS)
     const Span s = span_of(G, n, n_valid, blocks);
     if (s.first >= s.end) return;
     const int64_t pos0 = __ldg(start + s.b);
-    uint2 codes[BATCH];
-    uint32_t scale[BATCH];
-    int64_t to[BATCH];  // group of out, < 0: none
+    for (int64_t first = s.first; first < s.end; first += s.step) {
+        uint2 codes[BATCH];
+        uint32_t scale[BATCH];
+        int64_t to[BATCH];  // group of out, < 0: none
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) {
-        const int64_t at = s.first + k * THREADS + threadIdx.x;
-        to[k] = -1;
-        if (at >= s.end) continue;
-        const int64_t i = at / G;
-        const int g = (int)(at - i * G);
-        const int64_t cell = paged_row(pk, s.b, pos0 + i);
-        if (cell < 0) continue;
-        to[k] = ((int64_t)s.b * n + i) * G + g;
-        codes[k] = __ldg(reinterpret_cast<const uint2 *>(fp4 + cell * (C / 2) + g * 8));
-        scale[k] = MX ? __ldg(sf + cell * (C / 32) + (g >> 1)) : __ldg(sf + cell * G + g);
-    }
+        for (int k = 0; k < BATCH; k++) {
+            const int64_t at = first + k * THREADS + threadIdx.x;
+            to[k] = -1;
+            if (at >= s.end) continue;
+            const int64_t i = at / G;
+            const int g = (int)(at - i * G);
+            const int64_t cell = paged_row(pk, s.b, pos0 + i);
+            if (cell < 0) continue;
+            to[k] = ((int64_t)s.b * n + i) * G + g;
+            codes[k] = __ldg(reinterpret_cast<const uint2 *>(fp4 + cell * (C / 2) + g * 8));
+            scale[k] = MX ? __ldg(sf + cell * (C / 32) + (g >> 1)) : __ldg(sf + cell * G + g);
+        }
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) {
-        if (to[k] < 0) continue;
-        const MxScale s2 = MX ? mx_scale(scale[k]) : e4m3_scale(scale[k]);
-        uint4 *dst = reinterpret_cast<uint4 *>(out + to[k] * 16);
-        dst[0] = rows_bf16(codes[k].x, s2);
-        dst[1] = rows_bf16(codes[k].y, s2);
+        for (int k = 0; k < BATCH; k++) {
+            if (to[k] < 0) continue;
+            const MxScale s2 = MX ? mx_scale(scale[k]) : e4m3_scale(scale[k]);
+            uint4 *dst = reinterpret_cast<uint4 *>(out + to[k] * 16);
+            dst[0] = rows_bf16(codes[k].x, s2);
+            dst[1] = rows_bf16(codes[k].y, s2);
+        }
+        if constexpr (!WALK) break;
     }
 }
 
-// CTAs per sequence, and the grid.
-int grid_of(int B, int64_t groups, int &blocks, dim3 &grid) {
-    const int64_t per = (groups + PER_CTA - 1) / PER_CTA;
+// CTAs per sequence, the grid, and whether they walk.
+int grid_of(int B, int64_t groups, bool padded, int &blocks, dim3 &grid, bool &walk) {
+    int64_t per = (groups + PER_CTA - 1) / PER_CTA;
+    const int64_t most = ((int64_t)MOST * num_sms() + B - 1) / B;
+    walk = padded && per > most;
+    if (walk) per = most;
     if (per * B > INT32_MAX) return CSA2_ERR_SHAPE;
     blocks = (int)per;
     grid = dim3((unsigned)(per * B));
@@ -135,9 +148,10 @@ int append(const void *kv, int B, int n, int C, const int64_t *start, const int3
     if ((int64_t)B * n == 0) return CSA2_OK;
     dim3 grid;
     int blocks;
-    const int st = grid_of(B, (int64_t)n * (C / GC), blocks, grid);
+    bool walk;
+    const int st = grid_of(B, (int64_t)n * (C / GC), n_valid != nullptr, blocks, grid, walk);
     if (st != CSA2_OK) return st;
-    return launch_kernel(true, append_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream,
+    return launch_kernel(true, walk ? append_kernel<MX, true> : append_kernel<MX, false>, grid, dim3(THREADS), 0, (cudaStream_t)stream,
                          (const uint16_t *)kv, n, C, start, n_valid,
                          PagedKv{table, max_pages, page_size, n_pages}, blocks, fp4, sf);
 }
@@ -154,9 +168,10 @@ int gather(const uint8_t *fp4, const uint8_t *sf, const int32_t *table, int max_
     if ((int64_t)B * n == 0) return CSA2_OK;
     dim3 grid;
     int blocks;
-    const int st = grid_of(B, (int64_t)n * (C / 16), blocks, grid);
+    bool walk;
+    const int st = grid_of(B, (int64_t)n * (C / 16), n_valid != nullptr, blocks, grid, walk);
     if (st != CSA2_OK) return st;
-    return launch_kernel(true, gather_kernel<MX>, grid, dim3(THREADS), 0, (cudaStream_t)stream, fp4, sf,
+    return launch_kernel(true, walk ? gather_kernel<MX, true> : gather_kernel<MX, false>, grid, dim3(THREADS), 0, (cudaStream_t)stream, fp4, sf,
                          PagedKv{table, max_pages, page_size, n_pages}, start, n_valid, n, C, blocks,
                          (uint16_t *)out);
 }

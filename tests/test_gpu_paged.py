@@ -210,6 +210,29 @@ def test_append_equals_the_contiguous_append_on_any_bits(B, mx):
     assert torch.equal(a4.view(-1), b4.view(-1)) and torch.equal(asf.view(-1), bsf.view(-1))
 
 
+@pytest.mark.parametrize("mx", [False, True])
+def test_large_padded_batches(B, mx):
+    """Chunks that are mostly padding, large enough for a CTA to take several of its
+    sequence's pieces: the same bytes as one unpadded call per sequence."""
+    Bn, n, C, page = 3, 40000, 512, 33
+    valid = [39993, 0, 257]
+    x = torch.randn((Bn, n, C), generator=gen(n), device=DEV).to(torch.bfloat16)
+    start = i64([5, 0, 70])
+    table, n_pages = pool_of(Bn, n + 70, page, 3)
+    group = 32 if mx else 16
+    got, want = ([torch.full((n_pages, page, k), 0xAB, dtype=torch.uint8, device=DEV) for k in (C // 2, C // group)]
+                 for _ in range(2))
+    B.csa2_paged_kv_append_fp4(x, start, table, *got, n_valid=i32(valid), mx=mx)
+    out = torch.full((Bn, n, C), -7.0, dtype=torch.bfloat16, device=DEV)
+    B.csa2_paged_kv_gather(*got, table, start, out, n_valid=i32(valid), mx=mx)
+    for b, v in enumerate(valid):
+        row = x[b:b + 1, :v].contiguous()
+        B.csa2_paged_kv_append_fp4(row, start[b:b + 1], table[b:b + 1], *want, mx=mx)
+        B.csa2_paged_kv_gather(*want, table[b:b + 1], start[b:b + 1], row, mx=mx)
+        assert torch.equal(out[b, :v], row[0]) and bool((out[b, v:] == -7.0).all())
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_rows_without_a_page_are_skipped(B):
     page, C = 8, 64
     table = i32([[2, -1, 99, 0]])  # no page, a page outside the pool

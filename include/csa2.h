@@ -414,8 +414,8 @@ int csa2_attn_resident_clusters(int heads_per_cluster);
  *              positions [e page_size, (e + 1) page_size), negative if there is
  *              none. An entry outside [0, n_pages) counts as none in every call.
  *  ref         [n_pages] int32: how many sequences hold the page; 0 = free.
- *  page_size >= 1, max_pages >= 1, n_pages >= 1; page_size * max_pages and
- *  n_pages * page_size below 2^40.
+ *  page_size >= 1; max_pages and n_pages from 1 to 2^30; page_size * max_pages
+ *  and n_pages * page_size below 2^40.
  * A call over no rows, sequences or pairs is a no-op, whose arrays may be NULL.
  * Bytes that no append writes (the NaN codes of the scales) are not values: a
  * row that holds them gives unspecified results where it is read, and does no

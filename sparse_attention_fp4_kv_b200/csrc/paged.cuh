@@ -11,9 +11,11 @@ struct PagedKv {
     int max_pages, page_size, n_pages;
 };
 
-// Host-side checks shared by the paged calls.
+// Host-side checks shared by the paged calls. MAX_PAGES keeps an index and a grid's
+// stride on top of it within 32 bits.
+constexpr int MAX_PAGES = 1 << 30;
 inline bool paged_shape_ok(int max_pages, int page_size, int n_pages) {
-    return max_pages >= 1 && page_size >= 1 && n_pages >= 1 &&
+    return max_pages >= 1 && max_pages <= MAX_PAGES && page_size >= 1 && n_pages >= 1 && n_pages <= MAX_PAGES &&
            (int64_t)max_pages * page_size < (1ll << 40) && (int64_t)n_pages * page_size < (1ll << 40);
 }
 

@@ -411,7 +411,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     volatile int *abort = reinterpret_cast<volatile int *>(sm + L::ABORT_OFF);
     auto bar = [&](uint32_t i) { return base + L::BAR_OFF + 8u * i; };
     const int G = gridDim.x, cta = blockIdx.x;
-    grid_dep_launch();
 
     if (tid == 0) {
         mbar_init(bar(L::B_QFULL), LOAD_WARPS);
@@ -438,6 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
     if (warp == S_WARP) tmem_alloc(base + L::TADDR_OFF, L::COLS);
 
     grid_dep_wait();
+    grid_dep_launch();
     // ---- this CTA's share of the tiles: the prefix of the sequences' tiles, chunk by
     // chunk of THREADS of them; one chunk, and one pass, for any usual batch
     int *red = reinterpret_cast<int *>(sm + L::RED_OFF);

@@ -527,7 +527,7 @@ int free_list(const int32_t *ref, int n_pages, const Ws &w, const R &r, int n_re
 using namespace csa2;
 
 extern "C" size_t csa2_pages_workspace_size(int n_pages, int n) {
-    if (n_pages < 1 || n < 0) return 0;
+    if (n_pages < 1 || n_pages > MAX_PAGES || n < 0) return 0;
     return pages::layout(nullptr, n_pages, n).bytes;
 }
 

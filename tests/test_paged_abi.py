@@ -62,6 +62,7 @@ GATHER = dict(fp4=GOOD, sf=GOOD, table=GOOD, M=4, page=16, N=100, start=GOOD, va
     (NULL, dict(start=None)), (NULL, dict(table=None)), (NULL, dict(fp4=None)), (NULL, dict(sf=None)),
     (SHAPE, dict(B=-1)), (SHAPE, dict(n=-1)), (SHAPE, dict(C=40)), (SHAPE, dict(C=0)), (SHAPE, dict(C=8224)),
     (SHAPE, dict(M=0)), (SHAPE, dict(page=0)), (SHAPE, dict(N=0)), (SHAPE, dict(page=1 << 30, M=1 << 12)),
+    (SHAPE, dict(M=(1 << 30) + 1, page=1)), (SHAPE, dict(N=(1 << 30) + 1, page=1)),
     (SHAPE, dict(page=1 << 30, N=1 << 12)), (ALIGN, dict(fp4=ODD4)), (0, dict(B=0)), (0, dict(n=0))])
 def test_append_and_gather_refusals(B, mx, status, change):
     fmt = "mxfp4" if mx else "fp4"
@@ -88,7 +89,8 @@ def test_page_call_refusals(B):
         assert call(B, "csa2_pages_free", free, **{k: None}) == NULL
     assert call(B, "csa2_pages_free", free, F=-1) == SHAPE and call(B, "csa2_pages_free", free, F=0) == 0
     for name, good in (("csa2_pages_extend", ext), ("csa2_pages_fork", fork), ("csa2_pages_free", free)):
-        for change in (dict(S=-1), dict(M=0), dict(N=0), dict(page=0), dict(page=1 << 30, N=1 << 12)):
+        for change in (dict(S=-1), dict(M=0), dict(N=0), dict(page=0), dict(page=1 << 30, N=1 << 12),
+                       dict(M=(1 << 30) + 1, page=1), dict(N=(1 << 30) + 1, page=1)):
             assert call(B, name, good, **change) == SHAPE, (name, change)
     for name, good in (("csa2_pages_extend", ext), ("csa2_pages_fork", fork)):
         assert call(B, name, good, ws=None) == WS and call(B, name, good, wsb=need - 1) == WS
@@ -108,7 +110,7 @@ def test_copy_and_compact_refusals(B):
     comp = dict(table=GOOD, S=3, M=4, ref=GOOD, N=10, bufs=bufs, n=2, tout=GOOD, rout=GOOD, live=GOOD, ws=GOOD, wsb=need, stream=None)
     for k in ("table", "ref", "bufs", "tout", "rout", "live"):
         assert call(B, "csa2_pages_compact", comp, **{k: None}) == NULL
-    for change in (dict(S=-1), dict(M=0), dict(N=0), dict(n=-1), dict(n=17)):
+    for change in (dict(S=-1), dict(M=0), dict(N=0), dict(n=-1), dict(n=17), dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 1)):
         assert call(B, "csa2_pages_compact", comp, **change) == SHAPE
     assert call(B, "csa2_pages_compact", comp, ws=None) == WS and call(B, "csa2_pages_compact", comp, wsb=need - 4) == WS
     assert call(B, "csa2_pages_compact", comp, ws=ODD8) == ALIGN

@@ -13,14 +13,14 @@ namespace pa {
 // Joins the parts that the CTAs of a split (sequence, head group) pair left:
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. A warp takes 128 channels of
 // one head, four per lane, and 32 parts at a time: lane i reads part i's (m, l),
-// the weights go round by shuffles, eight parts' O are in flight. WIDE: the eight
-// warps of a block share one such piece of work and take parts in turn, for the few
-// pairs of a small batch, which are split over many CTAs; else each has its own.
-// Pairs without a key get zeros here, pairs within one CTA are already finished.
+// the weights go round by shuffles; the first parts' O are on the way before the
+// weights are known. A chain of loads, each as long as L2 takes: WIDE, the JW warps
+// of a block share one such piece of work and take parts in turn, else each has its
+// own. Pairs without a key get zeros here, pairs within one CTA are already finished.
 // Block 0 also sets the error word.
-constexpr int JW = 8;            // warps
+constexpr int EARLY = 4;         // parts
 constexpr int MAX_CTAS = 1024;   // of the attention kernel
-template <bool WIDE>
+template <int JW, bool WIDE>
 __global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int pitch, int G, int chunks, int work, int *err) {
     __shared__ float4 acc_s[JW][32];
     __shared__ float2 ml_s[JW];
@@ -57,6 +57,14 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int step = WIDE ? JW : 1, first = WIDE ? warp : 0;  // this warp's parts: first, first + step, ...
     for (int i0 = first; i0 < n; i0 += 32 * step) {
+        const int count = (n - i0 + step - 1) / step < 32 ? (n - i0 + step - 1) / step : 32;
+        const float *po = a.part_o + (int64_t)hh * pitch + c;
+        float4 x[EARLY];  // asked for before the weights are known
+#pragma unroll
+        for (int j = 0; j < EARLY; j++) {
+            x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < count) x[j] = *reinterpret_cast<const float4 *>(po + (int64_t)slot(i0 + j * step) * NH * pitch);
+        }
         const int mine = i0 + lane * step;
         float2 ml = make_float2(REF_NONE, 0.0f);
         if (mine < n) ml = *reinterpret_cast<const float2 *>(a.part_ml + ((int64_t)slot(mine) * NH + hh) * 2);
@@ -70,16 +78,22 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const Args a, int NH, int
         l = l * old + sum;
         o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
         m = top;
-        const int count = (n - i0 + step - 1) / step < 32 ? (n - i0 + step - 1) / step : 32;
-        const float *po = a.part_o + (int64_t)hh * pitch + c;
-#pragma unroll 8
-        for (int j = 0; j < count; j++) {
+#pragma unroll
+        for (int j = 0; j < EARLY; j++) {
             const float w = __shfl_sync(0xffffffffu, wt, j);
-            const float4 x = *reinterpret_cast<const float4 *>(po + (int64_t)slot(i0 + j * step) * NH * pitch);
-            o.x += w * x.x;
-            o.y += w * x.y;
-            o.z += w * x.z;
-            o.w += w * x.w;
+            o.x += w * x[j].x;
+            o.y += w * x[j].y;
+            o.z += w * x[j].z;
+            o.w += w * x[j].w;
+        }
+#pragma unroll 8
+        for (int j = EARLY; j < count; j++) {
+            const float w = __shfl_sync(0xffffffffu, wt, j);
+            const float4 y = *reinterpret_cast<const float4 *>(po + (int64_t)slot(i0 + j * step) * NH * pitch);
+            o.x += w * y.x;
+            o.y += w * y.y;
+            o.z += w * y.z;
+            o.w += w * y.w;
         }
     }
     if constexpr (WIDE) {
@@ -173,12 +187,18 @@ int decode(bool mx, const void *q, const uint8_t *fp4, const uint8_t *sf, const 
                  w.o};
     const int st = mx ? launch_paged_attn_mxfp4(a, nh, G, s) : launch_paged_attn_fp4(a, nh, G, s);
     if (st != CSA2_OK) return st;
-    // a block per piece of work while that leaves the SMs a few blocks each
-    if (work <= 16 * G)
-        return launch_kernel(true, join_kernel<true>, dim3((unsigned)work), dim3(JW * 32), 0, s, a, nh, pitch, G, chunks,
+    // Blocks of four warps fit beside an attention CTA and wait there for it. Up to
+    // 16 pieces of work per SM a block shares one. With 24 parts or more to a pair
+    // sixteen warps share it (attention and join, one sequence of 9000, 64 heads of
+    // 512: 18.0 us with 16 warps, 20.8 with 8, 23.5 with 4; 8 sequences of 1000: 22.4
+    // with 8, 18.3 with 4).
+    auto join = [&](auto kernel, int warps, int blocks) {
+        return launch_kernel(true, kernel, dim3((unsigned)blocks), dim3(warps * 32), 0, s, a, nh, pitch, G, chunks,
                              (int)work, w.err);
-    return launch_kernel(true, join_kernel<false>, dim3((unsigned)((work + JW - 1) / JW)), dim3(JW * 32), 0, s, a, nh,
-                         pitch, G, chunks, (int)work, w.err);
+    };
+    if (work > 16 * G) return join(join_kernel<4, false>, 4, (int)((work + 3) / 4));
+    if (B * groups <= G / 24) return join(join_kernel<16, true>, 16, (int)work);
+    return join(join_kernel<4, true>, 4, (int)work);
 }
 
 }  // namespace pa

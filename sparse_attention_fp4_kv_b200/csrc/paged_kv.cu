@@ -5,7 +5,8 @@
 // the contiguous append: a row of 512 channels is one warp, so its loads (32 B
 // per lane), code stores (8 B) and scale stores (1 B) are coalesced, and the
 // 32 lanes' table look-ups fall on one word. Bound by memory; what it takes is
-// loads in flight and CTAs that have work.
+// loads in flight and CTAs that have work. 65,536 rows of 512 (86 MB each way, 13.1 us
+// at the copy rate): append 24.9 us (MXFP4 17.4), read-back 17.1 (17.4).
 #include "fp4_rows.cuh"
 #include "kv_quant.cuh"
 #include "paged.cuh"

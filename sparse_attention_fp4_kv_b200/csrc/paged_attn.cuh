@@ -32,7 +32,7 @@
 // the ring), rows read whole lines at a time and a warp that stays together 280, two
 // issuing warps and bulk copies 268, the scout, which takes the walk and the
 // table out of the load warps, 238, loads past L1 229, one buffer of weights 223, a
-// prologue of one 32-bit scan 220. 128-key tiles
+// prologue of one 32-bit scan 218, a faster joining kernel 213. 128-key tiles
 // (M = 128 for S) leave room for one tile: 292. 16 load warps, at 72
 // registers, spill: 342.
 //

@@ -520,7 +520,8 @@ size_t csa2_pages_workspace_size(int n_pages, int n);
 /* Gives sequence s the pages of positions [0, want_len[s]): every entry
  * e < ceil(want_len[s] / page_size) of its row that has none takes a free page
  * (ref = 1), in the order of (s, e). Entries beyond max_pages and entries for
- * which no page is left stay without; n_failed counts the latter.
+ * which no page is left stay without; n_failed counts the latter (2^31 - 1 if
+ * there are more).
  *  want_len [S] int64 (device), n_failed [1] int32 (device). */
 int csa2_pages_extend(int32_t *page_table, int S, int max_pages, int32_t *ref, int n_pages,
                       int page_size, const int64_t *want_len, int32_t *n_failed, void *ws,

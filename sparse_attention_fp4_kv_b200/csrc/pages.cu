@@ -48,14 +48,15 @@ Ws layout(void *base, int n_pages, int n) {
     return w;
 }
 
-// Sum over the CTA's T threads, the same in all of them.
-__device__ __forceinline__ int block_sum(int v, int *smem) {
+// Sum over the CTA's threads, the same in all of them.
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, V *smem) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
     __syncthreads();
-    int t = (threadIdx.x & 31) < (blockDim.x >> 5) ? smem[threadIdx.x & 31] : 0;
+    V t = (threadIdx.x & 31) < (blockDim.x >> 5) ? smem[threadIdx.x & 31] : 0;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
     return t;
@@ -273,25 +274,29 @@ __global__ void __launch_bounds__(FT)
 }
 
 // ---------------------------------------------------------------- extend
+// Needs are summed in 64 bits: a table may lack more than 2^31 pages. What fails is
+// what is needed beyond the free pages; the last sequence's block counts it.
 __global__ void __launch_bounds__(FT)
     extend_kernel(int32_t *table, int32_t *ref, Extend x, const int32_t *head, const int32_t *list,
                   const int32_t *need, int32_t *n_failed) {
     __shared__ int smem[32];
+    __shared__ int64_t wide[32];
     grid_dep_wait();
     grid_dep_launch();
-    const int s = blockIdx.x;
-    if (need[s] == 0) return;
-    int64_t before = 0;  // entries of earlier sequences that need a page; may exceed int32
-    {
-        int64_t a = 0;
-        for (int k = threadIdx.x; k < s; k += FT) a += need[k];
-        const int lo = block_sum((int)(a & 0xFFFFFF), smem), hi = block_sum((int)(a >> 24), smem);
-        before = ((int64_t)hi << 24) + lo;
-    }
-    const int lim = pages_of(x.want[s], x.page_size, x.max_pages);
+    const int s = blockIdx.x, own = need[s];
+    const bool last = s == x.S - 1;
+    if (own == 0 && !last) return;
+    int64_t before = 0;  // entries of earlier sequences that need a page
+    for (int k = threadIdx.x; k < s; k += FT) before += need[k];
+    before = block_sum(before, wide);
     const int n_free = head[0];
+    if (last && threadIdx.x == 0) {
+        const int64_t failed = before + own - n_free;
+        *n_failed = failed <= 0 ? 0 : failed < INT32_MAX ? (int32_t)failed : INT32_MAX;
+    }
+    if (own == 0) return;
+    const int lim = pages_of(x.want[s], x.page_size, x.max_pages);
     int32_t *row = table + (int64_t)s * x.max_pages;
-    int failed = 0;
     for (int e0 = 0; e0 < lim; e0 += FT) {
         const int e = e0 + (int)threadIdx.x;
         bool miss = false;
@@ -302,18 +307,12 @@ __global__ void __launch_bounds__(FT)
         int total;
         const int64_t rank = before + block_scan(miss, smem, total);
         before += total;
-        if (miss) {
-            if (rank < n_free) {
-                const int p = list[rank];
-                row[e] = p;
-                ref[p] = 1;
-            } else {
-                failed++;
-            }
+        if (miss && rank < n_free) {
+            const int p = list[rank];
+            row[e] = p;
+            ref[p] = 1;
         }
     }
-    failed = block_sum(failed, smem);
-    if (threadIdx.x == 0 && failed) atomicAdd(n_failed, failed);
 }
 
 // ---------------------------------------------------------------- free

@@ -294,6 +294,24 @@ def test_extend(B, S, M, N, page):
     same(pool, table, refc)
 
 
+@pytest.mark.parametrize("S,lacking", [(200, (1 << 23) + 1), (258, (1 << 23) + 1)])
+def test_extend_of_very_many_entries(B, S, lacking):
+    """Up to more than 2^31 entries without a page: the first take what there is,
+    nothing else is written, and the count of the others stops at 2^31 - 1."""
+    M, N, page = lacking + 3, 5, 7
+    table = torch.full((S, M), -1, dtype=torch.int32, device=DEV)
+    table[2, 1] = 4
+    refc, want, failed = i32([0, 0, 0, 0, 1]), i64([lacking * page - 2] * S), i32([-9])
+    want[0] = 2 * page
+    B.csa2_pages_extend(table, refc, want, page, failed)
+    # lacking: two in the first row, all but one in the third; four pages were free
+    assert int(failed) == min(2 ** 31 - 1, 2 + (S - 1) * lacking - 1 - 4)
+    assert refc.tolist() == [1] * N
+    assert table[0, :3].tolist() == [0, 1, -1] and table[1, :3].tolist() == [2, 3, -1] and table[2, :3].tolist() == [-1, 4, -1]
+    table[0, :2] = table[1, :2] = table[2, 1] = -1
+    assert int(table.max()) == int(table.min()) == -1
+
+
 @pytest.mark.parametrize("S,M,N,page,F", [(2, 1, 3, 1, 1), (9, 7, 60, 16, 3), (90, 33, 4096, 8, 30),
                                           (200, 40, 9000, 7, 66), (60, 2100, 16385, 64, 20)])
 def test_fork_and_free(B, S, M, N, page, F):

@@ -75,6 +75,78 @@ def attend(q, fp4, sf, table, lens, scale, win=0, sink=0, mx=False):
     return torch.stack(outs), torch.stack(lses), torch.stack(bounds), torch.stack(lse_bounds)
 
 
+def shares(tiles, ctas):
+    """How the attention divides its list of tiles: [(sequence and head group, first
+    tile, behind the last)] of each CTA, where `tiles` has the tiles of each pair in
+    the list's order."""
+    total = sum(tiles)
+    ctas = min(ctas, total)
+    got, pair, at = [], 0, 0
+    for c in range(ctas):
+        left, own = (c + 1) * total // ctas - c * total // ctas, []
+        while left:
+            if at == tiles[pair]:
+                pair, at = pair + 1, 0
+                continue
+            n = min(left, tiles[pair] - at)
+            own.append((pair, at, at + n))
+            at, left = at + n, left - n
+        got.append(own)
+    return got
+
+
+def online(x, rows, moved, tile=64, far=8.0):
+    """The attention of one share as the kernel goes about it, in fp64: x [H][n] scores
+    in units of log2, rows [n][C]. The reference is the first tile's maximum and moves
+    when a score exceeds it by `far`; moved(o, l, factor) gives the sums after that.
+    (out, lse, moves of each head)"""
+    ref, count = None, torch.zeros(x.shape[0], dtype=torch.int64)
+    for j in range(0, x.shape[1], tile):
+        s, v = x[:, j:j + tile], rows[j:j + tile]
+        m = s.amax(-1)
+        if ref is None:
+            ref, l, o = m, torch.zeros_like(m), torch.zeros((x.shape[0], rows.shape[1]), dtype=x.dtype)
+        else:
+            up = m > ref + far
+            now = torch.where(up, m, ref)
+            o, l = moved(o, l, torch.exp2(ref - now))
+            ref, count = now, count + up
+        w = torch.exp2(s - ref[:, None])
+        o, l = o + w @ v, l + w.sum(-1)
+    return o / l[:, None], (ref + l.log2()) * math.log(2.0), count
+
+
+LEVELS = [m * 2.0 ** k for k in range(-1, 6) for m in (1.0, 1.5)] + [64.0]
+
+
+def stepped(kind, n, H, C, mx, g, device):
+    """(queries [1][H][C], codes [n][C/2], scales, softmax scale) whose scores go by
+    steps: the first 32 channels of key j all hold one value, the rest is random and no
+    query looks at it. Scores reach 64 to 120."""
+    i = torch.arange(n, device=device)
+    if kind == "rising":
+        level = i * len(LEVELS) // n
+    elif kind == "falling":
+        level = (n - 1 - i) * len(LEVELS) // n
+    elif kind == "saw":  # up and down from tile to tile, and up on the whole
+        t = i // 64
+        level = (t * 3 // 2 + 7 * (t % 2) - 4 * (t % 3 == 2).long()).clamp(0, len(LEVELS) - 1)
+    else:  # a single high key in every second tile, each above the last
+        level = torch.where(i % 128 == 73, 6 + 2 * (i // 128), 0).clamp(max=len(LEVELS) - 1)
+    v = torch.tensor(LEVELS, dtype=torch.float64, device=device)[level]
+    e = torch.floor(torch.log2(v)).long()
+    group = 32 if mx else 16
+    codes = torch.randint(0, 256, (n, C // 2), generator=g, device=device, dtype=torch.uint8)
+    lo, hi = (122, 130) if mx else (0x20, 0x40)
+    sf = torch.randint(lo, hi, (n, C // group), generator=g, device=device, dtype=torch.uint8)
+    codes[:, :16] = torch.where(v > 1.25 * 2.0 ** e.double(), 0x33, 0x22).to(torch.uint8)[:, None]  # 1.5 or 1, twice a byte
+    sf[:, :32 // group] = (e + 127 if mx else (e + 7) << 3).to(torch.uint8)[:, None]
+    q = torch.zeros((1, H, C), device=device)
+    q[..., :32] = torch.randn((1, H, 32), generator=g, device=device).abs()
+    q *= (torch.linspace(0.8, 1.5, H, device=device)[:, None] * 25 / q.sum(-1, keepdim=True))
+    return q.to(torch.bfloat16), codes, sf, 0.05
+
+
 def rope(x, pos, freq, start, interleaved, inverse, gain):
     """fp64 rotation and its per-element error bound, without the rounding of the
     result: the reduced angle is off by at most pi 2^-25 (rounded to fp32), sin

@@ -581,6 +581,34 @@ def test_attention_split_and_batched(B, Bn, Hq, C, page, ctx):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def ctas():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("Hq,C", [(64, 512), (16, 512), (24, 128), (40, 320), (9, 224)])
+@pytest.mark.parametrize("kind", ["rising", "falling", "saw", "spikes"])
+def test_attention_references_move_within_a_share(B, kind, Hq, C, mx):
+    """Scores that climb by more than 2^8 several times inside one CTA's share of a
+    sequence, with one buffer of weights (64 heads of 512 channels) and with two. A
+    rescale that is left out exceeds the bound on these scores (test_paged_cases.py)."""
+    n, page, Bn = 704, 32, ctas() + 37
+    q, codes, sf_rows, scale = ref.stepped(kind, n, Hq, C, mx, gen(Hq + C), DEV)
+    x = (scale / math.log(2.0)) * (q[0].double() @ ref.dequant(codes, sf_rows, mx).T).cpu()
+    moves = torch.zeros(Hq, dtype=torch.int64)
+    for own in ref.shares([n // 64] * Bn, ctas()):
+        for _, lo, hi in own:
+            moves += ref.online(x[:, 64 * lo:64 * hi], torch.zeros((64 * (hi - lo), 1), dtype=torch.float64),
+                                lambda o, l, f: (o, l))[2]
+    assert int(moves.max()) == 0 if kind == "falling" else int(moves.min()) >= Bn
+    table, n_pages = pool_of(Bn, n, page, C)
+    fp4, sf = filled(n_pages, page, C, mx, C)
+    i = torch.arange(n, device=DEV)
+    rows = table.long()[:, i // page] * page + i % page
+    fp4.flatten(0, 1)[rows], sf.flatten(0, 1)[rows] = codes, sf_rows
+    attend(B, q.expand(Bn, Hq, C).contiguous(), fp4, sf, table, i64([n] * Bn), scale=scale, mx=mx, what=kind)
+
+
 def test_offsets_past_32_bits(B):
     """A pool of over 4 GB of codes, a sequence on its last pages."""
     C, page = 512, 64

@@ -586,6 +586,31 @@ def ctas():
 
 
 @pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("C,page", [(96, 33), (224, 64), (352, 17), (480, 5), (512, 64)])
+@pytest.mark.parametrize("Hq", [11, 27, 50, 67])
+def test_attention_of_many_tiles_a_cta(B, Hq, C, page, mx):
+    """Every width of head groups and of rows in both formats, ten tiles and more to a
+    CTA: long sequences whose shares go round the ring of tiles, and short ones, several
+    to a CTA, between them."""
+    r = np.random.RandomState(Hq + C)
+    lens = [60001, 0, 1] + [int(v) for v in r.randint(0, 700, 60)] + [64, 65, 24000] + [int(v) for v in r.randint(0, 200, 30)]
+    share = ref.shares([-(-n // 64) for n in lens for _ in range(-(-Hq // 64))], ctas())
+    assert min(sum(b - a for _, a, b in own) for own in share) >= 10 and max(len(own) for own in share) >= 3
+    need = [-(-n // page) for n in lens]
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device=DEV)
+    n_pages = sum(need) + 3
+    perm = torch.randperm(n_pages, generator=gen(C), device=DEV).to(torch.int32)
+    for b, k in enumerate(need):
+        table[b, :k] = perm[sum(need[:b]):sum(need[:b]) + k]
+    fp4, sf = filled(n_pages, page, C, mx, C + Hq)
+    q = (1.5 * torch.randn((len(lens), Hq, C), generator=gen(Hq), device=DEV)).to(torch.bfloat16)
+    a = attend(B, q, fp4, sf, table, i64(lens), mx=mx)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    B.csa2_paged_attn_decode(q, fp4, sf, table, i64(lens), out, 1 / math.sqrt(C), lse=lse, mx=mx)
+    assert torch.equal(a[0], out) and torch.equal(a[1], lse)
+
+
+@pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("Hq,C", [(64, 512), (16, 512), (24, 128), (40, 320), (9, 224)])
 @pytest.mark.parametrize("kind", ["rising", "falling", "saw", "spikes"])
 def test_attention_references_move_within_a_share(B, kind, Hq, C, mx):
@@ -607,6 +632,76 @@ def test_attention_references_move_within_a_share(B, kind, Hq, C, mx):
     rows = table.long()[:, i // page] * page + i % page
     fp4.flatten(0, 1)[rows], sf.flatten(0, 1)[rows] = codes, sf_rows
     attend(B, q.expand(Bn, Hq, C).contiguous(), fp4, sf, table, i64([n] * Bn), scale=scale, mx=mx, what=kind)
+
+
+@pytest.mark.parametrize("Hq,C", [(64, 512), (8, 128), (17, 160), (23, 320)])
+@pytest.mark.parametrize("win,sink", [(1, 0), (128, 4), (100, 300), (4096, 1), (5, 1 << 40), (300, 129)])
+def test_attention_window_and_first_tokens_mx(B, Hq, C, win, sink):
+    lens = [0, 1, 5, 127, 128, 129, 132, 133, 400, 1000, 5000]
+    page = 16
+    table, n_pages = pool_of(len(lens), 5008, page, win & 0xFFFF)
+    fp4, sf = filled(n_pages, page, C, True, C + sink % 1000)
+    q = torch.randn((len(lens), Hq, C), generator=gen(win & 0xFFFF), device=DEV).to(torch.bfloat16)
+    attend(B, q, fp4, sf, table, i64(lens), win=win, sink=sink, mx=True)
+
+
+@pytest.mark.parametrize("Hq,C", [(64, 512), (16, 256)])
+def test_attention_nan_query_stays_in_its_head_mx(B, Hq, C):
+    page = 64
+    table, n_pages = pool_of(2, 640, page, 1)
+    fp4, sf = filled(n_pages, page, C, True, 1)
+    q = torch.randn((2, Hq, C), generator=gen(1), device=DEV).to(torch.bfloat16)
+    lens = i64([600, 333])
+    clean, clean_lse = attend(B, q, fp4, sf, table, lens, mx=True)
+    q[0, 5, 7] = float("nan")
+    q[1, Hq - 4, 0] = float("inf")
+    out, lse = torch.empty_like(q), torch.empty((2, Hq), device=DEV)
+    B.csa2_paged_attn_decode(q, fp4, sf, table, lens, out, 1 / math.sqrt(C), lse=lse, mx=True)
+    keep = torch.ones((2, Hq), dtype=torch.bool, device=DEV)
+    keep[0, 5] = keep[1, Hq - 4] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
+    assert out[0, 5].isnan().all() and out[1, Hq - 4].isnan().all()
+
+
+@pytest.mark.parametrize("Bn,Hq,C,page,ctx", [(1, 64, 512, 64, 70001), (3, 8, 128, 48, 30011), (400, 64, 512, 16, 33),
+                                               (1300, 80, 32, 16, 130)])
+def test_attention_split_and_batched_mx(B, Bn, Hq, C, page, ctx):
+    r = np.random.RandomState(Bn)
+    lens = [ctx] + [int(r.randint(0, ctx + 1)) for _ in range(Bn - 1)]
+    table, n_pages = pool_of(Bn, ctx, page, Bn)
+    fp4, sf = filled(n_pages, page, C, True, Bn)
+    q = (1.5 * torch.randn((Bn, Hq, C), generator=gen(Bn), device=DEV)).to(torch.bfloat16)
+    a = attend(B, q, fp4, sf, table, i64(lens), mx=True)
+    b = attend(B, q, fp4, sf, table, i64(lens), mx=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_two_calls_over_disjoint_keys_are_joined_by_their_lse(B, mx):
+    """Each call sees every second page (a sequence among them whose second half is
+    empty); out = sum_i exp(lse_i - lse) out_i with lse = ln sum_i exp(lse_i)."""
+    C, Hq, page = 256, 24, 16
+    lens, scale = [900, 33, 7, 2000], 0.05
+    table, n_pages = pool_of(4, 2000, page, 9)
+    fp4, sf = filled(n_pages, page, C, mx, 9)
+    q = (2 * torch.randn((4, Hq, C), generator=gen(9), device=DEV)).to(torch.bfloat16)
+    want, want_lse, _, _ = ref.attend(q, fp4, sf, table, lens, scale, mx=mx)
+    parts = []
+    for odd in (0, 1):
+        half = table.clone()
+        half[:, 1 - odd::2] = -1
+        out, lse = attend(B, q, fp4, sf, half, i64(lens), scale=scale, mx=mx)
+        exact, _, bound, lse_bound = ref.attend(q, fp4, sf, half, lens, scale, mx=mx)
+        parts.append((out.double(), lse.double(), exact, bound, lse_bound))
+    lse = torch.logsumexp(torch.stack([p[1] for p in parts]), 0)
+    off = torch.stack([p[4] for p in parts]).amax(0)
+    weight = [torch.exp(p[1] - lse)[..., None] for p in parts]
+    joined = sum(w * p[0] for w, p in zip(weight, parts))
+    # a part is off by its own bound, its weight by a factor of exp(+- 2 off); off is far below 1
+    bound = sum(w * (p[3] + 3 * off[..., None] * (p[2].abs() + p[3])) for w, p in zip(weight, parts))
+    assert float(off.max()) < 0.01
+    assert ((joined - want).abs() <= bound * (1 + 4 * off[..., None]) + 1e-30).all()
+    assert ((lse - want_lse).abs() <= off).all()
 
 
 def test_offsets_past_32_bits(B):

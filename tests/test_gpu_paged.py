@@ -210,6 +210,32 @@ def test_append_equals_the_contiguous_append_on_any_bits(B, mx):
     assert torch.equal(a4.view(-1), b4.view(-1)) and torch.equal(asf.view(-1), bsf.view(-1))
 
 
+def test_append_codes_of_every_value_under_every_scale(B):
+    """The FP4 append takes its codes from products, not quotients: every bf16 value of
+    up to six times the scale, for each of the 126 scales, gives the oracle's codes (IEEE
+    division)."""
+    every = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    scales = ref.scale_table(False, "cpu")[1:127]
+    groups = []
+    for s in scales:
+        x = every[every.double().abs() <= 6 * s]  # NaN is not
+        x = torch.cat([x, x[:-x.numel() % 15]]).view(-1, 15)
+        groups.append(torch.cat([torch.full((x.shape[0], 1), float(6 * s), dtype=torch.bfloat16), x], 1))
+        assert float(groups[-1][0, 0]) == float(6 * s)
+    x = torch.cat(groups)
+    x = torch.cat([x, x[:-x.shape[0] % 32]]).view(1, -1, 512).contiguous().to(DEV)
+    n = x.shape[1]
+    a4, asf = (torch.zeros((1, n, k), dtype=torch.uint8, device=DEV) for k in (256, 32))
+    b4, bsf = (torch.zeros((n, 1, k), dtype=torch.uint8, device=DEV) for k in (256, 32))
+    B.csa2_kv_append_fp4(x, i64([0]), a4, asf)
+    B.csa2_paged_kv_append_fp4(x, i64([0]), torch.arange(n, device=DEV, dtype=torch.int32)[None], b4, bsf)
+    codes, sf = oracle.fp4_quantize(bf16_np(x))
+    assert set(np.unique(sf)) == set(range(1, 127))
+    for got4, got_sf in ((a4, asf), (b4, bsf)):
+        assert np.array_equal(got4.cpu().numpy().reshape(codes.shape), codes)
+        assert np.array_equal(got_sf.cpu().numpy().reshape(sf.shape), sf)
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_large_padded_batches(B, mx):
     """Chunks that are mostly padding, large enough for a CTA to take several of its

@@ -3,8 +3,9 @@
 //
 //   S^T[key, head]  = K Q^T        M = 64 keys, N = heads, K = channels
 //   O^T[chan, head] += V^T P^T     M = 128 channels, N = heads, K = 64 keys
-// with K = V = the dequantized rows. Keys and channels lie on the MMAs' 128 rows
-// because a decode query has 64 heads or fewer, and M = 64 runs at half rate.
+// with K = V = the dequantized rows. Keys and channels lie on the MMAs' rows, the
+// heads of a group (16, 32 or 64; more heads are several groups) on their columns.
+// S has M = 64, which runs at half rate: with 128 keys only one tile would fit.
 //
 // Work: every sequence is cut into tiles of 64 visible keys; the tiles of all
 // (sequence, head group) pairs form one list that is divided evenly over the
@@ -32,9 +33,9 @@
 // the ring), rows read whole lines at a time and a warp that stays together 280, two
 // issuing warps and bulk copies 268, the scout, which takes the walk and the
 // table out of the load warps, 238, loads past L1 229, one buffer of weights 223, a
-// prologue of one 32-bit scan 218, a faster joining kernel 213. 128-key tiles
-// (M = 128 for S) leave room for one tile: 292. 16 load warps, at 72
-// registers, spill: 342.
+// prologue of one 32-bit scan 218, a faster joining kernel 216 (205 in a replayed
+// graph). 128-key tiles (M = 128 for S) leave room for one tile: 292. 16 load warps,
+// at 72 registers, spill: 342.
 //
 // Softmax: out = sum 2^(x_j - r) v_j / sum 2^(x_j - r) for any reference r. r is
 // the head's maximum of its first tile and moves only when a score exceeds it
@@ -49,9 +50,12 @@
 // they round at 2^-25 absolute (2^-38 of it). Weights are rounded to f16: 2^-11
 // relative, an eighth of the output's own bf16 rounding; they are kept below
 // 2^15 by an offset of 7 in the exponent, so that weights down to 2^-21 of the
-// reference keep all bits and those below 2^-32 vanish. E8M0 scales exceed f16's
-// range: rows and queries are bf16 (exact), and the weights are two bf16 parts
-// (16 bits), which costs a second P V.
+// reference keep all bits and those below 2^-32 vanish. The sum of weights is taken
+// before they are rounded (its logarithm is the lse). What the rounding leaves is
+// 3e-5 to 1.6e-4 of the output (2-norm) beside 1.65e-3 for the output's own, and
+// changes 2 to 8 % of the outputs' bf16 values. E8M0 scales exceed f16's range:
+// rows and queries are bf16 (exact), and the weights are two bf16 parts (16 bits),
+// which costs a second P V: 8 sequences of 128K take 306 us, with E4M3 scales 205.
 #pragma once
 
 #include "fp4_rows.cuh"
@@ -369,7 +373,7 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
     return sdesc_sw<6>(addr, 16, 256);
 }
 
-// What the load warps tell the other roles about a tile, beside its keys.
+// What the scout tells the other roles about a tile, beside its keys.
 struct TileInfo {
     int b, g;   // sequence and head group
     int flags;  // kLast, kWhole, and the 16-key steps of P V
@@ -529,7 +533,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
             }
             const float *qf = reinterpret_cast<const float *>(sm + L::QF_OFF) + (seg % QF_RING) * NH + part * NG + hq * NC;
             const float *rq = ref + hq * NC;
-            // the step's barrier orders the load warps' writes of valid, info and qf
+            // the step's barrier carries on what the scout wrote before the load warps'
+            // arrival (valid, info), and the load warps' qf
             ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS), ur.phase, abort) && ok;
             const uint32_t vi = (uint32_t)k % VALID_RING;
             const TileInfo info = read_info(base + L::INFO_OFF, vi);
@@ -954,7 +959,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const Args a) {
         Ring<L::NP> pr;
         Ring<L::NT> ur;
         for (int k = 0; k < n_tiles && all_ok(ok); k++) {
-            // the softmax warps' barrier carries the load warps' info on to here
+            // this barrier carries the scout's info on to here
             ok = wait_bar(bar(L::B_UFULL + ur.i * L::NS), ur.phase, abort) && ok;
             const int flags = read_info(base + L::INFO_OFF, (uint32_t)k % VALID_RING).flags, steps = flags >> 8;
             const bool last = flags & kLast;

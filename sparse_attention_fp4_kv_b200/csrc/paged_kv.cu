@@ -4,9 +4,13 @@
 // row comes from its sequence's page table. One lane per scale group, as in
 // the contiguous append: a row of 512 channels is one warp, so its loads (32 B
 // per lane), code stores (8 B) and scale stores (1 B) are coalesced, and the
-// 32 lanes' table look-ups fall on one word. Bound by memory; what it takes is
-// loads in flight and CTAs that have work. 65,536 rows of 512 (86 MB each way, 13.1 us
-// at the copy rate): append 24.9 us (MXFP4 17.4), read-back 17.1 (17.4).
+// 32 lanes' table look-ups fall on one word. 262,144 rows of 512 (344 MB each way,
+// 52.5 us at the copy rate): MXFP4 append 62.4 us and read-back 64 to 65 are bound by
+// memory, by loads in flight and CTAs that have work. The FP4 append, 92.0 us, is
+// bound by instructions: 2.4 times those of the MXFP4 form (a scale, its reciprocal, a
+// row look-up and a 64-bit division per 16 channels instead of 32, and a product, two
+// clamps and two integer steps per channel), 80 % of the issue slots and 37 % of
+// DRAM's rate. 65,536 rows: 23.3 us (MXFP4 15.8), read-back 17.3.
 #include "fp4_rows.cuh"
 #include "kv_quant.cuh"
 #include "paged.cuh"

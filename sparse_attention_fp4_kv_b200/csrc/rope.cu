@@ -3,14 +3,16 @@
 // y = R(a) x per channel pair, a = pos * inv_freq. The angle of a far position
 // (1M tokens x 1 radian) needs more bits than fp32 has, so its turns
 // pos * inv_freq / 2pi are taken in fp64, reduced to [-1/2, 1/2] there, and only
-// the reduced angle goes to the fp32 sincospi. One fp64 product and one
-// sincospi per (token, pair) serve all heads of the token.
+// the reduced angle goes to the fp32 sincospi. Two fp64 products and one sincospi
+// per (token, pair) of a CTA's tile serve all its heads.
 //
 // Bound by memory: each element is read once and written once. A CTA takes a
 // tile of rows (one row = one head of one token), 16 bytes per thread and
 // access; its cos/sin table goes to shared memory while its first loads are in
 // flight. 4096 x 64 x 512 fp32 (1.07 GB): 161 us, 6.7 TB/s; 69,632 rows of 512 bf16
-// (143 MB): 25.5 us, 5.6 TB/s; 4 tokens x 64 heads: 2.6 us.
+// (143 MB): 25.6 us, 5.6 TB/s; 4 tokens x 64 heads: 2.5 us. In place, 64 channels
+// of 512: the 69,632 rows 20.8 us (18 MB, 2.8 us at the copy rate; what
+// bounds it was not looked into), 4096 x 64 rows 16.9 in bf16 (67 MB), 24.6 in fp32 (134 MB).
 #include "common.cuh"
 
 #include <cuda_bf16.h>
@@ -243,8 +245,8 @@ int launch(Args a, bool half, cudaStream_t s) {
     a.ncopy = vec ? rest / N : rest;
     // rows of a tile: two batches of 16-byte accesses per thread
     int want = 2 * BATCH * THREADS / (a.nrot + a.ncopy);
-    // fewer where a small call would leave SMs idle (4 tokens x 64 heads: 5.2 us with 8
-    // CTAs, 3.8 with 16)
+    // fewer where a small call would leave SMs idle (4 tokens x 64 heads of 512: 3.1 us
+    // with 8 CTAs of 32 rows, 2.4 with one row a CTA)
     const int64_t spread = a.T * a.H / (2 * num_sms());
     if (spread < want) want = (int)spread;
     const int rows = want < 1 ? 1 : want;

@@ -259,8 +259,8 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-// try_wait with a suspend-time hint (ns): returns at the phase completion or
-// after about the hint.
+// try_wait with a suspend-time hint (ns): the thread sleeps until the phase of the
+// given parity completes or about `ns` pass.
 __device__ __forceinline__ bool try_wait_hint(uint32_t bar, uint32_t parity, uint32_t ns) {
     uint32_t done;
     asm volatile(
@@ -275,24 +275,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// mbarrier.try_wait with a suspend-time hint (ns): the thread sleeps until the
-// phase of the given parity completes or about `ns` pass.
-__device__ __forceinline__ bool mbar_try_wait_ns(uint32_t bar, uint32_t parity, uint32_t ns) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return done != 0;
-}
 // Wait for the phase of the given parity, sleeping in try_wait between checks;
 // false when `limit_ns` of global time pass first.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; it++) {
-        if (mbar_try_wait_ns(bar, parity, 100000u)) return true;
+        if (try_wait_hint(bar, parity, 100000u)) return true;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) {
             t0 = now;
